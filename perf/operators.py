@@ -317,60 +317,62 @@ def plain_clip(s):
 
 # ------------------------------------------------------------------ the library's calls
 
-def workspace(s, nbytes):
-    """The program's workspace, made at its first pass and zeroed once."""
+def workspace(nbytes):
+    """A program's workspace, zeroed once."""
     from communication_overlap_amd import ovl
-    if "workspace" not in s:
-        s["workspace"] = torch.empty(max(16, nbytes), device="cuda", dtype=torch.uint8)
-        ovl.ovl_flags_reset(None, 0, s["workspace"], s["workspace"].numel())
-    return s["workspace"]
+    ws = torch.empty(max(16, nbytes), device="cuda", dtype=torch.uint8)
+    ovl.ovl_flags_reset(None, 0, ws, ws.numel())
+    return ws
 
 
 def own_linear(s):
     from communication_overlap_amd import ovl
-    c = s["case"]
     if "desc" not in s:
+        c = s["case"]
         s["desc"] = ovl.gemm_epilogue_desc(c["m"], c["n"], c["k"], act=c["act"], out_type=c["out"],
                                            res_type=c["residual"] or "bf16")
-    ws = workspace(s, ovl.gemm_epilogue_workspace_bytes(s["desc"]))
-    ovl.gemm_epilogue_run(s["desc"], s["a"], s["b"], s["bias"], s["residual"], s["out"], s["z"], ws)
-    return {"out": s["out"], "z": s["z"]} if c["keep_z"] else {"out": s["out"]}
+        s["ws"] = workspace(ovl.gemm_epilogue_workspace_bytes(s["desc"]))
+    ovl.gemm_epilogue_run(s["desc"], s["a"], s["b"], s["bias"], s["residual"], s["out"], s["z"], s["ws"])
+    return {"out": s["out"], "z": s["z"]} if s["z"] is not None else {"out": s["out"]}
 
 
 def own_grad(s):
     from communication_overlap_amd import ovl
-    c = s["case"]
     if "desc" not in s:
+        c = s["case"]
         s["desc"] = ovl.gemm_epilogue_grad_desc(c["m"], c["n"], c["k"], act_in=c["act"], da_type=c["da"],
                                                 db_type=c["db"])
-    ws = workspace(s, ovl.gemm_epilogue_grad_workspace_bytes(s["desc"]))
+        s["ws"] = workspace(ovl.gemm_epilogue_grad_workspace_bytes(s["desc"]))
     ovl.gemm_epilogue_grad_run(s["desc"], s["dz"], s["a"], s["b"], s["z_in"], s["da"], s["db"], s["db_in"],
-                               s["dbias"], s["dbias_in"], ws)
+                               s["dbias"], s["dbias_in"], s["ws"])
     result = {"da": s["da"], "db": s["db"]}
-    if c["dbias"]:
+    if s["dbias"] is not None:
         result["dbias"] = s["dbias"]
     return result
 
 
 def own_moe(s):
     from communication_overlap_amd import ovl
-    c = s["case"]
     if "desc" not in s:
+        c = s["case"]
         s["desc"] = ovl.moe_layer_desc(c["tokens"], c["hidden"], c["inter"], c["experts"], s["topk"].shape[1],
                                        act=c["act"], gated=c["gated"], w_type=c["weights"], out_type=c["out"],
                                        norm_topk=True)
-    ws = workspace(s, ovl.moe_layer_workspace_bytes(s["desc"]))
+        s["ws"] = workspace(ovl.moe_layer_workspace_bytes(s["desc"]))
     ovl.moe_layer_run(s["desc"], s["x"], s["router"], s["topk"], s["gates"], s["w1"], s["s1"], s["w2"], s["s2"],
-                      s["out"], ws)
-    return {"out": s["out"], "topk": s["topk"], "gates": s["gates"]} if c["route"] else {"out": s["out"]}
+                      s["out"], s["ws"])
+    if s["router"] is not None:
+        return {"out": s["out"], "topk": s["topk"], "gates": s["gates"]}
+    return {"out": s["out"]}
 
 
 def own_clip(s):
     from communication_overlap_amd import ovl
-    if "table" not in s:
-        s["table"] = workspace(s, ovl.grad_clip_workspace_bytes(len(s["src"])))
-        ovl.grad_clip_table(s["src"], s["dst"], s["table"])
-    ovl.grad_norm_clip_run(len(s["src"]), s["table"], s["case"]["max_norm"], s["norm"])
+    if "plan" not in s:
+        s["plan"] = ovl.grad_clip_plan(s["src"], s["dst"])
+        s["ws"] = workspace(s["plan"].workspace_bytes)
+        ovl.grad_clip_upload(s["plan"], s["ws"])
+    ovl.grad_norm_clip_run(s["plan"], s["case"]["max_norm"], s["norm"], s["ws"])
     return {"norm": s["norm"], "dst": s["dst"]}
 
 
