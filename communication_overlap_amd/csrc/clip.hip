@@ -1,0 +1,403 @@
+// Global gradient norm over many tensors, and clipping:
+//   norm = sqrt(sum over tensors and elements of g^2),
+//   coef = min(1, max_norm / (norm + 1e-6)),   dst = src * coef.
+// Squares and sums are float64 throughout (a float32 square overflows at
+// 1.8e19, and a float32 sum of 10^9 terms has lost its small ones); norm and
+// coef are rounded to float32 once.
+//
+// The tensors are numbered through in 16-byte slots, a tensor's first slot
+// being the one its first byte lies in (slots at multiples of 16 bytes of its
+// source).  Every wavefront owns one contiguous range of slots, finds its
+// first tensor with a 64-way search of the table, and walks on from there, so
+// one launch is balanced whatever the lengths are.  Only a tensor's first and
+// last slot can be partial; their elements go one per lane.
+//
+// Two launches: sums (one float64 a workgroup), then scaling, in which every
+// workgroup adds the sums up again, all in the same order.  The second walks
+// each range backwards with the same grid, so that it begins with what the
+// first read last, which the caches still hold.  What a single workgroup can
+// hold goes through one launch.
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "device.h"
+#include "host.h"
+
+namespace ovl {
+
+namespace {
+
+constexpr int kGcMaxGroups = 2048;  // workgroups of a launch, and float64 sums in the workspace
+constexpr int kGcUpload = 100;      // table entries that travel as one launch's arguments
+constexpr size_t kGcSums = kCounterBytes;
+constexpr size_t kGcTable = kGcSums + kGcMaxGroups * sizeof(double);
+
+struct GcEntry {
+  uint64_t src, dst;  // dst 0: the tensor only counts in the norm
+  int64_t first;      // number of its first slot
+  int64_t count;      // 2 * elements + (1 for float32, 0 for bf16)
+};
+
+struct GcUpload {
+  GcEntry e[kGcUpload];
+  GcEntry* table;
+  int32_t n;
+};
+
+struct GcArgs {
+  const GcEntry* table;  // tensors + 1 entries; the last holds the number of slots
+  double* sums;
+  float* norm;
+  int64_t tensors, slots;
+  int64_t per_wave;  // slots of a wavefront
+  float max_norm;
+};
+
+__global__ __launch_bounds__(64) void gc_upload_kernel(GcUpload u) {
+  for (int i = threadIdx.x; i < u.n; i += 64) u.table[i] = u.e[i];
+}
+
+__device__ inline float gc_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ inline float gc_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+// (Takes its word by value: a bit cast of a vector's element itself reads
+// element 0.)
+__device__ inline float gc_f32(uint32_t w) { return __builtin_bit_cast(float, w); }
+// float32 to bf16 bits, nearest with ties to even; NaN stays NaN.
+__device__ inline uint32_t gc_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+__device__ inline double gc_square_sum(u32x4 v, bool f32) {
+  double s = 0;
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double d = gc_f32(v[i]);
+      s += d * d;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double a = gc_lo(v[i]), b = gc_hi(v[i]);
+      s += a * a;
+      s += b * b;
+    }
+  }
+  return s;
+}
+
+__device__ inline u32x4 gc_scaled(u32x4 v, bool f32, float coef) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = f32 ? __builtin_bit_cast(uint32_t, gc_f32(v[i]) * coef)
+               : gc_bf16(gc_lo(v[i]) * coef) | gc_bf16(gc_hi(v[i]) * coef) << 16;
+  return v;
+}
+
+// The last tensor whose first slot is <= v (the one that holds slot v:
+// tensors without slots share their first slot with the one behind them).
+__device__ inline int64_t gc_find(const GcEntry* table, int64_t tensors, int64_t v) {
+  int64_t lo = 0, n = tensors;
+  while (n > 1) {
+    const int64_t step = (n + 63) / 64, i = lane_id() * step;
+    const bool le = i < n && table[lo + i].first <= v;
+    const int below = __popcll(__ballot(le));  // >= 1: table[lo].first <= v
+    lo += (below - 1) * step;
+    n = min(step, n - (below - 1) * step);
+  }
+  return lo;
+}
+
+// One tensor's slots, seen from the wavefront.
+struct GcTensor {
+  uint64_t src, dst;
+  int64_t first, slots, count;
+  bool f32;
+  int head;  // bytes of slot 0 ahead of the tensor
+
+  __device__ GcTensor(const GcEntry* table, int64_t t) {
+    const GcEntry e = table[t];
+    src = e.src;
+    dst = e.dst;
+    first = e.first;
+    slots = table[t + 1].first - e.first;
+    count = e.count >> 1;
+    f32 = e.count & 1;
+    head = (int)(src & 15);
+  }
+  __device__ int shift() const { return f32 ? 2 : 1; }
+  // Whole slots are [whole0, whole1); slot 0 and the last may be partial.
+  __device__ int64_t whole0() const { return head ? 1 : 0; }
+  __device__ int64_t whole1() const { return (head + (count << shift())) >> 4; }
+  // Element of a partial slot that this lane holds, or -1.
+  __device__ int64_t edge(int64_t slot) const {
+    const int64_t i = ((slot * 16 - head) >> shift()) + lane_id();
+    return lane_id() < (16 >> shift()) && i >= 0 && i < count ? i : -1;
+  }
+  __device__ float load(int64_t i) const {
+    return f32 ? reinterpret_cast<const float*>(src)[i]
+               : gc_lo(reinterpret_cast<const uint16_t*>(src)[i]);
+  }
+  __device__ void store(int64_t i, float v) const {
+    if (f32)
+      reinterpret_cast<float*>(dst)[i] = v;
+    else
+      reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)gc_bf16(v);
+  }
+  __device__ const u32x4* vec() const { return reinterpret_cast<const u32x4*>(src - head); }
+};
+
+constexpr int kGcU = 4;  // 16-byte loads in flight per lane
+
+// Sum of squares over slots [v0, v1), this lane's share.
+__device__ inline double gc_sum_range(const GcArgs& a, int64_t v0, int64_t v1) {
+  double s = 0;
+  if (v0 >= v1) return s;
+  const int lane = lane_id();
+  for (int64_t t = uniform64(gc_find(a.table, a.tensors, v0)); v0 < v1; ++t) {
+    const GcTensor g(a.table, t);
+    const int64_t b = v0 - g.first, e = min(v1 - g.first, g.slots);
+    const int64_t w0 = max(b, g.whole0()), w1 = min(e, g.whole1());
+    if (b < g.whole0() && b < e) {
+      const int64_t i = g.edge(b);
+      const double d = i >= 0 ? g.load(i) : 0.f;
+      s += d * d;
+    }
+    const u32x4* p = g.vec();
+    int64_t i = w0 + lane;
+    for (; i + (kGcU - 1) * 64 < w1; i += kGcU * 64) {
+      u32x4 v[kGcU];
+#pragma unroll
+      for (int u = 0; u < kGcU; ++u) v[u] = p[i + u * 64];
+#pragma unroll
+      for (int u = 0; u < kGcU; ++u) s += gc_square_sum(v[u], g.f32);
+    }
+    for (; i < w1; i += 64) s += gc_square_sum(p[i], g.f32);
+    if (e > g.whole1() && e - 1 >= g.whole0() && b < e) {
+      const int64_t j = g.edge(e - 1);
+      const double d = j >= 0 ? g.load(j) : 0.f;
+      s += d * d;
+    }
+    v0 = g.first + e;
+  }
+  return s;
+}
+
+__device__ inline void gc_scale_slot(const GcTensor& g, int64_t i, u32x4 v, float coef, bool vec) {
+  if (vec) {
+    reinterpret_cast<u32x4*>(g.dst - g.head)[i] = gc_scaled(v, g.f32, coef);
+    return;
+  }
+  // dst lies differently within its 16 bytes than src: element by element.
+  const int64_t e0 = (i * 16 - g.head) >> g.shift();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (g.f32) {
+      g.store(e0 + k, gc_f32(v[k]) * coef);
+    } else {
+      g.store(e0 + 2 * k, gc_lo(v[k]) * coef);
+      g.store(e0 + 2 * k + 1, gc_hi(v[k]) * coef);
+    }
+  }
+}
+
+// dst = src * coef over slots [v0, v1), from the last to the first.
+__device__ inline void gc_scale_range(const GcArgs& a, int64_t v0, int64_t v1, float coef) {
+  if (v0 >= v1) return;
+  const int lane = lane_id();
+  for (int64_t t = uniform64(gc_find(a.table, a.tensors, v1 - 1)); v0 < v1; --t) {
+    const GcTensor g(a.table, t);
+    const int64_t b = max(v0 - g.first, (int64_t)0), e = v1 - g.first;
+    v1 = min(v1, g.first);
+    // In place with coef 1 nothing changes.
+    if (b >= e || !g.dst || (g.dst == g.src && coef == 1.f)) continue;
+    const bool vec = ((g.dst ^ g.src) & 15) == 0;
+    const int64_t w0 = max(b, g.whole0()), w1 = min(e, g.whole1());
+    if (e > g.whole1() && e - 1 >= g.whole0()) {
+      const int64_t j = g.edge(e - 1);
+      if (j >= 0) g.store(j, g.load(j) * coef);
+    }
+    const u32x4* p = g.vec();
+    int64_t i = w1 - 1 - lane;
+    for (; i - (kGcU - 1) * 64 >= w0; i -= kGcU * 64) {
+      u32x4 v[kGcU];
+#pragma unroll
+      for (int u = 0; u < kGcU; ++u) v[u] = p[i - u * 64];
+#pragma unroll
+      for (int u = 0; u < kGcU; ++u) gc_scale_slot(g, i - u * 64, v[u], coef, vec);
+    }
+    for (; i >= w0; i -= 64) gc_scale_slot(g, i, p[i], coef, vec);
+    if (b < g.whole0()) {
+      const int64_t j = g.edge(b);
+      if (j >= 0) g.store(j, g.load(j) * coef);
+    }
+  }
+}
+
+__device__ inline double gc_wave_sum(double s) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
+  return s;
+}
+
+// Sum over the workgroup's threads, the same bits in every thread.
+template <int NT>
+__device__ inline double gc_group_sum(double s, double* lds) {
+  s = gc_wave_sum(s);
+  if (lane_id() == 0) lds[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) s += lds[w];
+  return s;
+}
+
+__device__ inline float gc_coef(const GcArgs& a, double sum, bool first) {
+  const double norm = sqrt(sum);
+  if (first) *a.norm = (float)norm;
+  const double c = (double)a.max_norm / (norm + 1e-6);
+  return c >= 1.0 || isinf(a.max_norm) ? 1.f : (float)c;  // a NaN norm gives a NaN coefficient
+}
+
+__global__ __launch_bounds__(kThreads) void gc_norm_kernel(GcArgs a) {
+  __shared__ double lds[kThreads / 64];
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 64) + uniform(threadIdx.x >> 6);
+  const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
+  const double s = gc_group_sum<kThreads>(gc_sum_range(a, v0, v1), lds);
+  if (threadIdx.x == 0) a.sums[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kThreads) void gc_scale_kernel(GcArgs a) {
+  __shared__ double lds[kThreads / 64];
+  double s = 0;
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) s += a.sums[i];
+  s = gc_group_sum<kThreads>(s, lds);
+  const float coef = gc_coef(a, s, blockIdx.x == 0 && threadIdx.x == 0);
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 64) + uniform(threadIdx.x >> 6);
+  const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
+  gc_scale_range(a, v0, v1, coef);
+}
+
+constexpr int kGcOneThreads = 1024;
+
+__global__ __launch_bounds__(kGcOneThreads) void gc_one_kernel(GcArgs a) {
+  __shared__ double lds[kGcOneThreads / 64];
+  const int64_t w = uniform(threadIdx.x >> 6);
+  const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
+  const double s = gc_group_sum<kGcOneThreads>(gc_sum_range(a, v0, v1), lds);
+  gc_scale_range(a, v0, v1, gc_coef(a, s, threadIdx.x == 0));
+}
+
+}  // namespace
+
+}  // namespace ovl
+
+using namespace ovl;
+
+struct grad_clip_plan_s {
+  std::vector<GcEntry> table;  // tensors + 1
+};
+
+extern "C" ovl_status grad_clip_plan(const grad_clip_tensor* tensors, int64_t num, grad_clip_plan_t* out) {
+  if (!out) return OVL_EINVAL;
+  *out = nullptr;
+  if (num < 0 || (num && !tensors)) return OVL_EINVAL;
+  if (num > (1 << 20)) return OVL_EUNSUPPORTED;
+  try {
+    struct Span {
+      uint64_t lo, hi;
+      int64_t owner;
+      bool written;
+    };
+    std::vector<GcEntry> table;
+    std::vector<Span> spans;
+    table.reserve(num + 1);
+    int64_t slot = 0;
+    for (int64_t i = 0; i < num; ++i) {
+      const grad_clip_tensor& t = tensors[i];
+      if ((t.type != OVL_BF16 && t.type != OVL_F32) || t.reserved) return OVL_EINVAL;
+      if (t.count < 0) return OVL_ESHAPE;
+      if (t.count > (1ll << 40)) return OVL_EUNSUPPORTED;
+      const uint64_t src = reinterpret_cast<uint64_t>(t.src), dst = reinterpret_cast<uint64_t>(t.dst);
+      const uint64_t size = t.type == OVL_F32 ? 4 : 2, bytes = (uint64_t)t.count * size;
+      if (t.count && !src) return OVL_EINVAL;
+      if ((src | dst) & (size - 1)) return OVL_EALIGN;
+      table.push_back({src, dst, slot, 2 * t.count + (t.type == OVL_F32)});
+      if (!t.count) continue;
+      slot += (int64_t)(((src & 15) + bytes + 15) / 16);
+      if (dst != src) spans.push_back({src, src + bytes, i, false});
+      if (dst) spans.push_back({dst, dst + bytes, i, true});
+    }
+    table.push_back({0, 0, slot, 0});
+    // What is written may overlap nothing else that the call reads or writes
+    // (a tensor clipped in place is one span).
+    std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
+    uint64_t end_any = 0, end_written = 0;
+    for (const Span& s : spans) {
+      if (s.lo < end_written || (s.written && s.lo < end_any)) return OVL_EINVAL;
+      end_any = std::max(end_any, s.hi);
+      if (s.written) end_written = std::max(end_written, s.hi);
+    }
+    grad_clip_plan_s* p = new grad_clip_plan_s;
+    p->table.swap(table);
+    *out = p;
+  } catch (const std::bad_alloc&) {
+    return OVL_EUNSUPPORTED;
+  }
+  return OVL_OK;
+}
+
+extern "C" ovl_status grad_clip_plan_destroy(grad_clip_plan_t p) {
+  delete p;
+  return OVL_OK;
+}
+
+extern "C" size_t grad_clip_workspace_bytes(grad_clip_plan_t p) {
+  return p ? kGcTable + aligned_up(p->table.size() * sizeof(GcEntry), 256) : 0;
+}
+
+extern "C" ovl_status grad_clip_upload(grad_clip_plan_t p, void* workspace, hipStream_t stream) {
+  if (!p || !workspace) return OVL_EINVAL;
+  if (!aligned16(workspace)) return OVL_EALIGN;
+  GcUpload u = {};
+  GcEntry* table = reinterpret_cast<GcEntry*>(static_cast<uint8_t*>(workspace) + kGcTable);
+  for (size_t i = 0; i < p->table.size(); i += kGcUpload) {
+    u.n = (int32_t)std::min<size_t>(kGcUpload, p->table.size() - i);
+    std::copy_n(p->table.begin() + i, u.n, u.e);
+    u.table = table + i;
+    hipLaunchKernelGGL(gc_upload_kernel, dim3(1), dim3(64), 0, stream, u);
+    OVL_HIP_TRY(hipGetLastError());
+  }
+  return OVL_OK;
+}
+
+extern "C" ovl_status grad_norm_clip_run(grad_clip_plan_t p, float max_norm, float* norm, void* workspace,
+                                         hipStream_t stream) {
+  if (!p || !norm || !workspace) return OVL_EINVAL;
+  if (!(max_norm >= 0.f)) return OVL_EINVAL;  // negative or NaN
+  if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(norm) & 3u)) return OVL_EALIGN;
+  DeviceInfo di;
+  ovl_status st = current_device_info(&di);
+  if (st) return st;
+  GcArgs a = {};
+  a.table = reinterpret_cast<const GcEntry*>(static_cast<uint8_t*>(workspace) + kGcTable);
+  a.sums = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + kGcSums);
+  a.norm = norm;
+  a.tensors = (int64_t)p->table.size() - 1;
+  a.slots = p->table.back().first;
+  a.max_norm = max_norm;
+  if (a.slots <= 8192) {
+    a.per_wave = ceil_div(a.slots, kGcOneThreads / 64);
+    hipLaunchKernelGGL(gc_one_kernel, dim3(1), dim3(kGcOneThreads), 0, stream, a);
+    OVL_HIP_TRY(hipGetLastError());
+    return OVL_OK;
+  }
+  const int64_t groups =
+      std::min<int64_t>({kGcMaxGroups, (int64_t)di.cus * 8, ceil_div(a.slots, 64 * kGcU * (kThreads / 64))});
+  a.per_wave = ceil_div(a.slots, groups * (kThreads / 64));
+  hipLaunchKernelGGL(gc_norm_kernel, dim3((uint32_t)groups), dim3(kThreads), 0, stream, a);
+  OVL_HIP_TRY(hipGetLastError());
+  hipLaunchKernelGGL(gc_scale_kernel, dim3((uint32_t)groups), dim3(kThreads), 0, stream, a);
+  OVL_HIP_TRY(hipGetLastError());
+  return OVL_OK;
+}

@@ -1,0 +1,162 @@
+// What follows a product's float32 sums: bias, activation, residual, the
+// activation's derivative, and the rounding into the output's type.  All of
+// it is float32; an output is rounded once, to nearest with ties to even.
+#pragma once
+
+#include "device.h"
+#include "ovl.h"
+
+namespace ovl {
+
+__device__ inline float bf16_lo_f(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ inline float bf16_hi_f(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+__device__ inline uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+__device__ inline uint32_t bf16_pair(float a, float b) { return bf16_bits(a) | bf16_bits(b) << 16; }
+
+// 1 / (1 + exp(-x)): the hardware's exp2 and reciprocal, both within an ulp
+// or two; exp overflows to infinity, whose reciprocal is the right zero.
+__device__ inline float sigmoid_f(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
+}
+
+constexpr float kGeluR = 0.797884560802865356f;  // sqrt(2 / pi)
+constexpr float kGeluC = 0.044715f;
+
+// The tanh form of GELU, 0.5 z (1 + tanh u), is z sigmoid(2 u): no
+// cancellation where tanh is near -1.
+__device__ inline float act_f(float z, int kind) {
+  switch (kind) {
+    case OVL_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
+    case OVL_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.707106781186547524f));
+    case OVL_ACT_GELU_TANH: return z * sigmoid_f(2.f * kGeluR * (z + kGeluC * z * z * z));
+    case OVL_ACT_SILU: return z * sigmoid_f(z);
+    default: return z;
+  }
+}
+
+// d act / dz.  Beyond |z| = 32 every smooth one is 0 or 1 in float32; taking
+// that keeps infinity times zero out of the products below.
+__device__ inline float act_grad_f(float z, int kind) {
+  if (kind == OVL_ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+  if (kind == OVL_ACT_NONE) return 1.f;
+  const bool far = fabsf(z) > 32.f;
+  const float limit = z > 0.f ? 1.f : 0.f;
+  switch (kind) {
+    case OVL_ACT_GELU:
+      return far ? limit
+                 : 0.5f * (1.f + erff(z * 0.707106781186547524f)) +
+                       z * 0.398942280401432678f * __builtin_amdgcn_exp2f(-0.5f * 1.44269504088896341f * z * z);
+    case OVL_ACT_GELU_TANH: {
+      const float s = sigmoid_f(2.f * kGeluR * (z + kGeluC * z * z * z));
+      return far ? limit : s + z * s * (1.f - s) * (2.f * kGeluR * (1.f + 3.f * kGeluC * z * z));
+    }
+    default: {
+      const float s = sigmoid_f(z);
+      return far ? limit : s + z * s * (1.f - s);
+    }
+  }
+}
+
+// The same for eight values: one branch on the kind for all of them.
+__device__ inline void act8(float (&v)[8], int kind) {
+#define OVL_ACT8(K)                                    \
+  case K:                                              \
+    _Pragma("unroll") for (int c = 0; c < 8; ++c) v[c] = act_f(v[c], K); \
+    break;
+  switch (kind) {
+    OVL_ACT8(OVL_ACT_RELU)
+    OVL_ACT8(OVL_ACT_GELU)
+    OVL_ACT8(OVL_ACT_GELU_TANH)
+    OVL_ACT8(OVL_ACT_SILU)
+    default: break;
+  }
+#undef OVL_ACT8
+}
+
+// v *= act'(z).
+__device__ inline void act_grad8(float (&v)[8], const float (&z)[8], int kind) {
+#define OVL_ACT8(K)                                    \
+  case K:                                              \
+    _Pragma("unroll") for (int c = 0; c < 8; ++c) v[c] *= act_grad_f(z[c], K); \
+    break;
+  switch (kind) {
+    OVL_ACT8(OVL_ACT_RELU)
+    OVL_ACT8(OVL_ACT_GELU)
+    OVL_ACT8(OVL_ACT_GELU_TANH)
+    OVL_ACT8(OVL_ACT_SILU)
+    default: break;
+  }
+#undef OVL_ACT8
+}
+
+// Eight consecutive elements of a row in float32, from bf16 or float32.
+__device__ inline void load8(float (&v)[8], const void* p, int64_t i, int type) {
+  if (type == OVL_F32) {
+    const f32x4 a = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i)[0];
+    const f32x4 b = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i)[1];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[c] = a[c];
+      v[4 + c] = b[c];
+    }
+  } else {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[2 * c] = bf16_lo_f(w[c]);
+      v[2 * c + 1] = bf16_hi_f(w[c]);
+    }
+  }
+}
+
+__device__ inline void store8(const float (&v)[8], void* p, int64_t i, int type) {
+  if (type == OVL_F32) {
+    reinterpret_cast<f32x4*>(static_cast<float*>(p) + i)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4*>(static_cast<float*>(p) + i)[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    u32x4 w;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = bf16_pair(v[2 * c], v[2 * c + 1]);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = w;
+  }
+}
+
+// The epilogue of one product, columns n (a multiple of 8):
+//   z = sum + bias;  out = act(z) + residual;  z_out = bf16(z)
+// or, with z_in, out = sum * act'(z_in) (the gradient's), or with `add` a
+// float addend in out's type: out = sum + add.
+struct Epilogue {
+  void* out;
+  void* z_out;           // bf16, or null
+  const float* bias;     // [n], or null
+  const void* residual;  // or null
+  const void* z_in;      // bf16, or null: multiply by act'(z_in)
+  int64_t ld_out, ld_z, ld_res;  // ld_z: of z_out or z_in
+  int32_t out_type, res_type, act;
+};
+
+__device__ inline void epilogue8(const Epilogue& e, int64_t row, int64_t col, float (&v)[8]) {
+  if (e.bias) {
+    float b[8];
+    load8(b, e.bias, col, OVL_F32);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] += b[c];
+  }
+  if (e.z_out) store8(v, e.z_out, row * e.ld_z + col, OVL_BF16);
+  if (e.z_in) {
+    float z[8];
+    load8(z, e.z_in, row * e.ld_z + col, OVL_BF16);
+    act_grad8(v, z, e.act);
+  } else {
+    act8(v, e.act);
+  }
+  if (e.residual) {
+    float r[8];
+    load8(r, e.residual, row * e.ld_res + col, e.res_type);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] += r[c];
+  }
+  store8(v, e.out, row * e.ld_out + col, e.out_type);
+}
+
+}  // namespace ovl

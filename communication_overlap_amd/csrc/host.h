@@ -13,6 +13,12 @@ namespace ovl {
     if ((expr) != hipSuccess) return OVL_EHIP;    \
   } while (0)
 
+// The head of the feed-forward calls' workspaces: the error record, then
+// int32 arrival counters, zero between calls.  Nothing else lies there, so
+// that calls of different kinds and sizes may use one workspace in turn.
+constexpr size_t kCounterBytes = 16384;
+constexpr int32_t kCounters = (int32_t)(kCounterBytes - OVL_ERROR_RECORD_BYTES) / 4;
+
 constexpr uint64_t kDefaultSpinLimit = 1ull << 22;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, byref, c_char_p, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, Structure, byref, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libovl.so")
@@ -31,6 +31,11 @@ MODE_BARRIER = 3
 
 ERROR_RECORD_BYTES = 64
 
+BF16, F32, FP8 = 0, 1, 2
+TYPES = {"bf16": BF16, "f32": F32, "fp8": FP8}
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+
 EXPORTS = (
     "ag_gemm_plan", "ag_gemm_plan_destroy", "ag_gemm_num_units", "ag_gemm_flags_bytes",
     "ag_gemm_workspace_bytes", "ag_gemm_splits", "ag_gemm_run",
@@ -41,6 +46,9 @@ EXPORTS = (
     "ring_allreduce_flags_bytes", "ring_allreduce_workspace_bytes", "ring_allreduce_run",
     "fp8_quantize_rows", "a2a_dispatch_grouped_gemm_fp8_run", "ag_gemm_trace_bytes",
     "ag_gemm_row_tiles", "ag_gemm_tile_rows", "ag_gemm_consumer_order", "ag_gemm_run_noalloc",
+    "gemm_epilogue_workspace_bytes", "gemm_epilogue_run", "gemm_epilogue_grad_workspace_bytes",
+    "gemm_epilogue_grad_run", "moe_layer_workspace_bytes", "moe_layer_run",
+    "grad_clip_plan", "grad_clip_plan_destroy", "grad_clip_workspace_bytes", "grad_clip_upload", "grad_norm_clip_run",
 )
 
 
@@ -74,6 +82,25 @@ class A2aDesc(Structure):
 
 class RingDesc(Structure):
     _fields_ = [("ranks", c_int32), ("n", c_int64), ("tile", c_int64), ("flag_stride", c_int32)]
+
+
+class GemmEpilogueDesc(Structure):
+    _fields_ = [(f, c_int64) for f in ("m", "n", "k", "lda", "ldb", "ldo", "ldz", "ldr")] + \
+               [(f, c_int32) for f in ("act", "out_type", "res_type", "reserved")]
+
+
+class GemmEpilogueGradDesc(Structure):
+    _fields_ = [(f, c_int64) for f in ("m", "n", "k", "lda", "ldb", "lddz", "lddy", "ldz", "ldz_in", "ldda", "lddb")] + \
+               [(f, c_int32) for f in ("act", "act_in", "dy_type", "da_type", "db_type", "reserved")]
+
+
+class MoeLayerDesc(Structure):
+    _fields_ = [(f, c_int64) for f in ("tokens", "hidden", "inter")] + \
+               [(f, c_int32) for f in ("experts", "topk", "act", "gated", "w_type", "out_type", "norm_topk", "reserved")]
+
+
+class GradClipTensor(Structure):
+    _fields_ = [("src", c_void_p), ("dst", c_void_p), ("count", c_int64), ("type", c_int32), ("reserved", c_int32)]
 
 
 _lib = None
@@ -160,6 +187,28 @@ def lib() -> ctypes.CDLL:
                                                     c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
                                                     POINTER(Opts), c_void_p]
     L.a2a_dispatch_grouped_gemm_fp8_run.restype = st
+    L.gemm_epilogue_workspace_bytes.argtypes = [POINTER(GemmEpilogueDesc)]
+    L.gemm_epilogue_workspace_bytes.restype = c_size_t
+    L.gemm_epilogue_run.argtypes = [POINTER(GemmEpilogueDesc)] + [c_void_p] * 8
+    L.gemm_epilogue_run.restype = st
+    L.gemm_epilogue_grad_workspace_bytes.argtypes = [POINTER(GemmEpilogueGradDesc)]
+    L.gemm_epilogue_grad_workspace_bytes.restype = c_size_t
+    L.gemm_epilogue_grad_run.argtypes = [POINTER(GemmEpilogueGradDesc)] + [c_void_p] * 13
+    L.gemm_epilogue_grad_run.restype = st
+    L.moe_layer_workspace_bytes.argtypes = [POINTER(MoeLayerDesc)]
+    L.moe_layer_workspace_bytes.restype = c_size_t
+    L.moe_layer_run.argtypes = [POINTER(MoeLayerDesc)] + [c_void_p] * 11
+    L.moe_layer_run.restype = st
+    L.grad_clip_plan.argtypes = [POINTER(GradClipTensor), c_int64, POINTER(c_void_p)]
+    L.grad_clip_plan.restype = st
+    L.grad_clip_plan_destroy.argtypes = [c_void_p]
+    L.grad_clip_plan_destroy.restype = st
+    L.grad_clip_workspace_bytes.argtypes = [c_void_p]
+    L.grad_clip_workspace_bytes.restype = c_size_t
+    L.grad_clip_upload.argtypes = [c_void_p, c_void_p, c_void_p]
+    L.grad_clip_upload.restype = st
+    L.grad_norm_clip_run.argtypes = [c_void_p, c_float, c_void_p, c_void_p, c_void_p]
+    L.grad_norm_clip_run.restype = st
     _lib = L
     return L
 
@@ -385,6 +434,186 @@ def ring_allreduce_run(desc: RingDesc, inputs, outputs, flags, workspace, epoch:
     st = lib().ring_allreduce_run(byref(desc), _ptr_array(inputs), _ptr_array(outputs), _ptr(flags),
                                   _ptr(workspace), epoch, byref(o), _stream(stream))
     return _check(st, "ring_allreduce_run", raise_on_error)
+
+
+# ------------------------------------------------------------------ feed-forward layers
+
+def _act(act) -> int:
+    return ACTS[act] if isinstance(act, str) else act
+
+
+def _type(t) -> int:
+    return TYPES[t] if isinstance(t, str) else t
+
+
+class _Buffers:
+    """Marshals the buffers of one call of the feed-forward calls.  A tensor
+    has to lie on the current device, hold elements of the right size and be
+    as large as the call takes it to be (dense, or a two-dimensional view with
+    the descriptor's row stride); raw addresses pass unchecked."""
+
+    def __init__(self, where: str):
+        import torch
+        self.where = where
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+    def refuse(self, name: str, why: str):
+        raise OvlError(OVL_EINVAL, f"{self.where}: {name} {why}")
+
+    def __call__(self, name: str, t, size: int, rows: int, cols: int, ld: int = 0):
+        if t is None or isinstance(t, int):
+            return t
+        if not t.is_cuda or t.get_device() != self.device:
+            self.refuse(name, "is not on the current device")
+        if t.element_size() != size:
+            self.refuse(name, f"has elements of {t.element_size()} bytes, not {size}")
+        ld = ld or cols
+        if t.is_contiguous():
+            if rows > 0 and t.numel() < (rows - 1) * ld + cols:
+                self.refuse(name, "is too small")
+        elif not (t.dim() == 2 and t.stride(1) == 1 and t.stride(0) == ld and t.shape[0] >= rows
+                  and t.shape[1] >= cols):
+            self.refuse(name, "is neither dense nor a matrix with the descriptor's row stride")
+        return t.data_ptr()
+
+
+_SIZE = {BF16: 2, F32: 4, FP8: 1}
+
+
+def gemm_epilogue_desc(m, n, k, act="none", out_type="bf16", res_type="bf16", lda=0, ldb=0, ldo=0, ldz=0,
+                       ldr=0) -> GemmEpilogueDesc:
+    return GemmEpilogueDesc(m, n, k, lda, ldb, ldo, ldz, ldr, _act(act), _type(out_type), _type(res_type), 0)
+
+
+def gemm_epilogue_workspace_bytes(desc: GemmEpilogueDesc) -> int:
+    return lib().gemm_epilogue_workspace_bytes(byref(desc))
+
+
+def gemm_epilogue_run(desc: GemmEpilogueDesc, a, b, bias, residual, out, z, workspace, stream=None,
+                      raise_on_error: bool = True) -> int:
+    """out = act(a @ b + bias) + residual; z: the rounded pre-activation (bias, residual and z may be None)."""
+    buf = _Buffers("gemm_epilogue_run")
+    m, n, k = desc.m, desc.n, desc.k
+    st = lib().gemm_epilogue_run(
+        byref(desc), buf("a", a, 2, m, k, desc.lda), buf("b", b, 2, k, n, desc.ldb), buf("bias", bias, 4, 1, n),
+        buf("residual", residual, _SIZE.get(desc.res_type, 1), m, n, desc.ldr),
+        buf("out", out, _SIZE.get(desc.out_type, 1), m, n, desc.ldo), buf("z", z, 2, m, n, desc.ldz),
+        _workspace(buf, workspace, lib().gemm_epilogue_workspace_bytes, desc), _stream(stream))
+    return _check(st, "gemm_epilogue_run", raise_on_error)
+
+
+def _workspace(buf, workspace, nbytes, desc):
+    if workspace is None or isinstance(workspace, int):
+        return workspace
+    return buf("workspace", workspace, 1, 1, nbytes(byref(desc)))
+
+
+def gemm_epilogue_grad_desc(m, n, k, act="none", act_in="none", dy_type="bf16", da_type="bf16", db_type="f32", lda=0,
+                            ldb=0, lddz=0, lddy=0, ldz=0, ldz_in=0, ldda=0, lddb=0) -> GemmEpilogueGradDesc:
+    return GemmEpilogueGradDesc(m, n, k, lda, ldb, lddz, lddy, ldz, ldz_in, ldda, lddb, _act(act), _act(act_in),
+                                _type(dy_type), _type(da_type), _type(db_type), 0)
+
+
+def gemm_epilogue_grad_workspace_bytes(desc: GemmEpilogueGradDesc) -> int:
+    return lib().gemm_epilogue_grad_workspace_bytes(byref(desc))
+
+
+def gemm_epilogue_grad_run(desc: GemmEpilogueGradDesc, dz, a, b, z_in, da, db, db_in, dbias, dbias_in, workspace,
+                           dy=None, z=None, stream=None, raise_on_error: bool = True) -> int:
+    """da = (dz @ b^T) * act_in'(z_in), db = db_in + a^T @ dz, dbias = dbias_in + column sums of dz; with the
+    descriptor's act, dz = dy * act'(z) is computed first.  Any of da, db, dbias may be None."""
+    buf = _Buffers("gemm_epilogue_grad_run")
+    m, n, k = desc.m, desc.n, desc.k
+    db_size = _SIZE.get(desc.db_type, 1)
+    st = lib().gemm_epilogue_grad_run(
+        byref(desc), buf("dy", dy, _SIZE.get(desc.dy_type, 1), m, n, desc.lddy), buf("z", z, 2, m, n, desc.ldz),
+        buf("dz", dz, 2, m, n, desc.lddz), buf("a", a, 2, m, k, desc.lda), buf("b", b, 2, k, n, desc.ldb),
+        buf("z_in", z_in, 2, m, k, desc.ldz_in), buf("da", da, _SIZE.get(desc.da_type, 1), m, k, desc.ldda),
+        buf("db", db, db_size, k, n, desc.lddb), buf("db_in", db_in, db_size, k, n, desc.lddb),
+        buf("dbias", dbias, 4, 1, n), buf("dbias_in", dbias_in, 4, 1, n),
+        _workspace(buf, workspace, lib().gemm_epilogue_grad_workspace_bytes, desc), _stream(stream))
+    return _check(st, "gemm_epilogue_grad_run", raise_on_error)
+
+
+def moe_layer_desc(tokens, hidden, inter, experts, topk, act="silu", gated=True, w_type="bf16", out_type="bf16",
+                   norm_topk=True) -> MoeLayerDesc:
+    return MoeLayerDesc(tokens, hidden, inter, experts, topk, _act(act), int(gated), _type(w_type), _type(out_type),
+                        int(norm_topk), 0)
+
+
+def moe_layer_workspace_bytes(desc: MoeLayerDesc) -> int:
+    return lib().moe_layer_workspace_bytes(byref(desc))
+
+
+def moe_layer_run(desc: MoeLayerDesc, x, router, topk_idx, gates, w1, w1_scale, w2, w2_scale, out, workspace,
+                  stream=None, raise_on_error: bool = True) -> int:
+    """The whole layer for a few tokens; with a router, topk_idx and gates are written, else read."""
+    buf = _Buffers("moe_layer_run")
+    t, h, i, e, k = desc.tokens, desc.hidden, desc.inter, desc.experts, desc.topk
+    n1, w = (2 * i if desc.gated else i), _SIZE.get(desc.w_type, 1)
+    st = lib().moe_layer_run(
+        byref(desc), buf("x", x, 2, t, h), buf("router", router, 2, h, e), buf("topk_idx", topk_idx, 4, t, k),
+        buf("gates", gates, 4, t, k), buf("w1", w1, w, e * h, n1), buf("w1_scale", w1_scale, 4, e, n1),
+        buf("w2", w2, w, e * i, h), buf("w2_scale", w2_scale, 4, e, h),
+        buf("out", out, _SIZE.get(desc.out_type, 1), t, h),
+        _workspace(buf, workspace, lib().moe_layer_workspace_bytes, desc), _stream(stream))
+    return _check(st, "moe_layer_run", raise_on_error)
+
+
+class GradClipPlan:
+    """Owns a grad_clip_plan_t, and keeps the tensors it was made of."""
+
+    def __init__(self, src, dst=None):
+        """src: tensors (bfloat16 or float32); dst: as many (None entries: only in the norm), or None to clip in place."""
+        import torch
+        dst = list(src) if dst is None else list(dst)
+        src = list(src)
+        if len(src) != len(dst):
+            raise OvlError(OVL_EINVAL, "grad_clip_plan: as many outputs as inputs")
+        buf = _Buffers("grad_clip_plan")
+        arr = (GradClipTensor * max(1, len(src)))()
+        for i, (s, d) in enumerate(zip(src, dst)):
+            if s.dtype not in (torch.bfloat16, torch.float32) or (d is not None and d.dtype != s.dtype):
+                buf.refuse(f"tensor {i}", "is not bfloat16 or float32, or its output is of another type")
+            if not s.is_contiguous() or (d is not None and (not d.is_contiguous() or d.numel() != s.numel())):
+                buf.refuse(f"tensor {i}", "is not dense, or its output is of another size")
+            n = s.numel()
+            arr[i] = GradClipTensor(buf(f"tensor {i}", s, s.element_size(), 1, n) or None,
+                                    buf(f"output {i}", d, s.element_size(), 1, n) or None, n,
+                                    F32 if s.dtype == torch.float32 else BF16, 0)
+        self.tensors = (src, dst)
+        h = c_void_p()
+        _check(lib().grad_clip_plan(arr, len(src), byref(h)), "grad_clip_plan", True)
+        self.handle = h
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and h.value and _lib is not None:
+            _lib.grad_clip_plan_destroy(h)
+            self.handle = None
+
+    @property
+    def workspace_bytes(self) -> int:
+        return lib().grad_clip_workspace_bytes(self.handle)
+
+
+def grad_clip_plan(src, dst=None) -> GradClipPlan:
+    return GradClipPlan(src, dst)
+
+
+def grad_clip_upload(plan: GradClipPlan, workspace, stream=None, raise_on_error: bool = True) -> int:
+    buf = _Buffers("grad_clip_upload")
+    ws = buf("workspace", workspace, 1, 1, plan.workspace_bytes)
+    return _check(lib().grad_clip_upload(plan.handle, ws, _stream(stream)), "grad_clip_upload", raise_on_error)
+
+
+def grad_norm_clip_run(plan: GradClipPlan, max_norm: float, norm, workspace, stream=None,
+                       raise_on_error: bool = True) -> int:
+    """norm (float32 [1]) = the global norm; every dst = src * min(1, max_norm / (norm + 1e-6))."""
+    buf = _Buffers("grad_norm_clip_run")
+    st = lib().grad_norm_clip_run(plan.handle, max_norm, buf("norm", norm, 4, 1, 1),
+                                  buf("workspace", workspace, 1, 1, plan.workspace_bytes), _stream(stream))
+    return _check(st, "grad_norm_clip_run", raise_on_error)
 
 
 # ------------------------------------------------------------------ flags, errors, copy

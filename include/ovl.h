@@ -497,6 +497,177 @@ ovl_status ring_allreduce_run(const ring_desc* desc, const float* const* in, flo
                               hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Feed-forward layers on one rank: the products around the overlapped ones,
+ * with what follows them fused into their epilogues, their gradients, the
+ * experts' layer for a few tokens, and the norm of the gradients.
+ *
+ * These calls use no flags and no epochs: each is complete in stream order.
+ * Their workspaces need no reset between calls (each call says whether it
+ * needs one before the first) and may be shared by any calls that do not
+ * overlap in time, captured ones included.  Row strides (ld*) count elements, 0 standing for a
+ * dense row; they are multiples of 8, at most 2^20, and what lies between a
+ * row's end and the next row is neither read nor written.  Outputs may not
+ * overlap inputs, but for the cases named at each call.
+ * ---------------------------------------------------------------------- */
+enum { OVL_BF16 = 0, OVL_F32 = 1, OVL_FP8 = 2 /* E4M3 codes with scales */ };
+
+/* Activations.  GELU: z (1 + erf(z / sqrt 2)) / 2; GELU_TANH: z (1 + tanh(
+ * sqrt(2 / pi) (z + 0.044715 z^3))) / 2; SILU: z / (1 + exp(-z)).  RELU's
+ * derivative at 0 is 0.  NaN stays NaN. */
+enum { OVL_ACT_NONE = 0, OVL_ACT_RELU = 1, OVL_ACT_GELU = 2, OVL_ACT_GELU_TANH = 3, OVL_ACT_SILU = 4 };
+
+/* ------------------------------------------------------------------------
+ * Product with bias, activation and residual:
+ *   z = a @ b + bias,   out = act(z) + residual
+ * in float32 from bf16 operands; out (and z where it is asked for) is rounded
+ * once.  m = 1 (a decoded token) up to 2^20 rows.
+ * ---------------------------------------------------------------------- */
+typedef struct gemm_epilogue_desc {
+  int64_t m, n, k;                 /* m >= 0; n, k >= 8, multiples of 8; at most 2^20 each */
+  int64_t lda, ldb, ldo, ldz, ldr; /* row strides of a, b, out, z and residual */
+  int32_t act;                     /* OVL_ACT_* */
+  int32_t out_type, res_type;      /* OVL_BF16 or OVL_F32 */
+  int32_t reserved;                /* 0 */
+} gemm_epilogue_desc;
+
+/* 0 for an invalid desc. */
+size_t gemm_epilogue_workspace_bytes(const gemm_epilogue_desc* desc);
+
+/* a: bf16 [m][k]; b: bf16 [k][n]; bias: float32 [n] or NULL; residual [m][n]
+ * of res_type or NULL; out [m][n] of out_type; z: bf16 [m][n] or NULL, the
+ * rounded pre-activation, kept for the gradient.  residual may be out itself
+ * (same type and stride).  With m = 0 nothing is read or written and the row
+ * buffers may be NULL.
+ * workspace: gemm_epilogue_workspace_bytes(desc) bytes, zeroed once before
+ * its first use (ovl_flags_reset).  Errors: EINVAL, ESHAPE, EALIGN;
+ * EUNSUPPORTED for a size over 2^20 or an operand (a, b) over 1 GiB. */
+ovl_status gemm_epilogue_run(const gemm_epilogue_desc* desc, const void* a, const void* b,
+                             const float* bias, const void* residual, void* out, void* z,
+                             void* workspace, hipStream_t stream);
+
+/* Gradient of the product above (m, n, k, a and b as there):
+ *   dz    = bf16(dy * act'(z))                       [m][n], if act is not NONE
+ *   da    = (dz @ b^T) * act_in'(z_in)               [m][k]
+ *   db    = db_in + a^T @ dz                         [k][n]
+ *   dbias = dbias_in + the sum of dz's rows          [n]
+ * The gradient of the residual is dy itself.  With act NONE, dz is an input:
+ * the incoming gradient.  act_in (NONE: no factor) is the activation that
+ * made `a` from z_in, the layer before this one, so that da is that layer's
+ * dz and a feed-forward block's backward pass runs no separate activation
+ * kernel.  Sums are float32 and each output is rounded once; dz is bf16
+ * because the matrix units take it as such. */
+typedef struct gemm_epilogue_grad_desc {
+  int64_t m, n, k;
+  int64_t lda, ldb, lddz, lddy, ldz, ldz_in, ldda, lddb;
+  int32_t act;      /* not NONE: dz is computed from dy and z */
+  int32_t act_in;
+  int32_t dy_type;  /* OVL_BF16 or OVL_F32, each: */
+  int32_t da_type;
+  int32_t db_type;  /* also db_in's */
+  int32_t reserved; /* 0 */
+} gemm_epilogue_grad_desc;
+
+size_t gemm_epilogue_grad_workspace_bytes(const gemm_epilogue_grad_desc* desc);
+
+/* dy [m][n] of dy_type and z bf16 [m][n]: only with act (else NULL).  dz: bf16
+ * [m][n], written with act, else read.  z_in: bf16 [m][k], if act_in is not
+ * NONE and da is asked for (else NULL).  da, db, dbias: each may be NULL (not
+ * computed); db_in [k][n] of db_type and dbias_in [n] may be NULL (nothing to
+ * add) or the outputs themselves (accumulation in place; strides as db's).
+ * dz may be dy, and da may be z_in (bf16, equal strides).  With m = 0 db and dbias are
+ * db_in and dbias_in, or zero, and the row buffers may be NULL.
+ * workspace: gemm_epilogue_grad_workspace_bytes(desc) bytes, no reset needed.
+ * Errors as for gemm_epilogue_run (operands: a, b, dz). */
+ovl_status gemm_epilogue_grad_run(const gemm_epilogue_grad_desc* desc, const void* dy, const void* z,
+                                  void* dz, const void* a, const void* b, const void* z_in, void* da,
+                                  void* db, const void* db_in, float* dbias, const float* dbias_in,
+                                  void* workspace, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A whole mixture-of-experts layer for a few tokens (decoding; the dispatch
+ * above is made for thousands): routing, the experts' two products and the
+ * gate-weighted sum, on the weights in the layout of the dispatch calls.
+ *   logits = x @ router (64-bit sums); choice j of token t is the expert with
+ *   the j-th largest logit (ties: the lower id; NaN counts as smaller than
+ *   every number); gates = softmax(logits) at the choices, over all experts,
+ *   or with norm_topk over the chosen ones;
+ *   u = x[t] @ w1[e];  h = act(u[0:inter]) * u[inter:2 inter] (gated) or
+ *   act(u);  out[t] = sum over j, ascending, of gates[t][j] * (h @ w2[e]).
+ * With router NULL the caller's topk_idx and gates are read instead; ids
+ * outside [0, experts) (an expert of another rank) contribute nothing, and an
+ * id may stand more than once.  Sums and h are float32 (h enters the matrix
+ * units as two bf16 terms, 16 bits, for bf16 output and three, 24 bits, for
+ * float32); out is rounded once.  Results do not depend on timing.
+ * ---------------------------------------------------------------------- */
+typedef struct moe_layer_desc {
+  int64_t tokens;   /* 0..128 */
+  int64_t hidden;   /* multiple of 8 (FP8: 16), 8..2^16 */
+  int64_t inter;    /* likewise */
+  int32_t experts;  /* 1..256 */
+  int32_t topk;     /* 1..8, <= experts */
+  int32_t act;      /* OVL_ACT_* */
+  int32_t gated;    /* 0: w1 has inter columns, 1: 2 * inter (gate, then up) */
+  int32_t w_type;   /* OVL_BF16 or OVL_FP8 */
+  int32_t out_type; /* OVL_BF16 or OVL_F32 */
+  int32_t norm_topk;/* 0 or 1 */
+  int32_t reserved; /* 0 */
+} moe_layer_desc;
+
+size_t moe_layer_workspace_bytes(const moe_layer_desc* desc);
+
+/* x: bf16 [tokens][hidden]; router: bf16 [hidden][experts] (dense, any number
+ * of experts) or NULL; topk_idx: int32 [tokens][topk] and gates: float32
+ * [tokens][topk], written with a router, else read.  n1 = gated ? 2 inter :
+ * inter.  OVL_BF16: w1 bf16 [experts][hidden][n1], w2 bf16
+ * [experts][inter][hidden], scales NULL.  OVL_FP8: w1 E4M3 codes
+ * [experts][n1][hidden] with w1_scale float32 [experts][n1], w2 codes
+ * [experts][hidden][inter] with w2_scale float32 [experts][hidden] (the
+ * layout of a2a_dispatch_grouped_gemm_fp8_run and fp8_quantize_rows).
+ * out: [tokens][hidden] of out_type.
+ * workspace: moe_layer_workspace_bytes(desc) bytes, zeroed once before its
+ * first use (ovl_flags_reset).  Errors: EINVAL, ESHAPE, EALIGN; EUNSUPPORTED
+ * past the limits above. */
+ovl_status moe_layer_run(const moe_layer_desc* desc, const void* x, const void* router,
+                         int32_t* topk_idx, float* gates, const void* w1, const float* w1_scale,
+                         const void* w2, const float* w2_scale, void* out, void* workspace,
+                         hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Global gradient norm and clipping (what follows the all-reduce of the
+ * gradients): norm = sqrt of the sum of all squares, in 64 bits; coef =
+ * min(1, max_norm / (norm + 1e-6)), 1 where max_norm is infinite;
+ * dst = src * coef, rounded once into the tensor's type.
+ * A norm that is infinite gives coef 0, a NaN norm coef NaN, as the formula has it.
+ * ---------------------------------------------------------------------- */
+typedef struct grad_clip_tensor {
+  const void* src;  /* device; aligned to its element only */
+  void* dst;        /* device, likewise; src itself (in place), or NULL: only counted in the norm */
+  int64_t count;    /* elements, >= 0 (0: src may be NULL) */
+  int32_t type;     /* OVL_BF16 or OVL_F32, of src and dst */
+  int32_t reserved; /* 0 */
+} grad_clip_tensor;
+
+typedef struct grad_clip_plan_s* grad_clip_plan_t;
+
+/* Validates `num` tensors (HOST array, 0..2^20 of them) and builds an
+ * immutable host-only plan that holds their addresses.  Errors: EINVAL (a
+ * dst that overlaps another tensor's dst or any src but its own equal one
+ * among them), ESHAPE, EALIGN, EUNSUPPORTED. */
+ovl_status grad_clip_plan(const grad_clip_tensor* tensors, int64_t num, grad_clip_plan_t* out);
+ovl_status grad_clip_plan_destroy(grad_clip_plan_t plan);
+size_t grad_clip_workspace_bytes(grad_clip_plan_t plan);
+
+/* Writes the plan's table into `workspace` (kernels on `stream`, which carry
+ * the entries in their arguments); once for any number of runs of this plan
+ * on this workspace, ordered before them. */
+ovl_status grad_clip_upload(grad_clip_plan_t plan, void* workspace, hipStream_t stream);
+
+/* norm: device float32.  max_norm >= 0, infinite for the norm alone (a dst
+ * other than src is still written, as a copy).  Errors: EINVAL, EALIGN. */
+ovl_status grad_norm_clip_run(grad_clip_plan_t plan, float max_norm, float* norm, void* workspace,
+                              hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Flags, errors, measurement.
  * ---------------------------------------------------------------------- */
 

@@ -21,3 +21,5 @@ from .dispatch import dispatch_layout, dispatch, grouped_gemm, grouped_gemm_rows
 from .combine import combine, combine_positions  # noqa: F401
 from .ring import ring_allreduce, allreduce_sum, ring_chunk_bounds  # noqa: F401
 from .fp8 import e4m3_decode, e4m3_encode, quantize_rows, dispatch_fp8, grouped_gemm_fp8  # noqa: F401
+from .feedforward import (act, act_grad, gemm_epilogue, gemm_epilogue_grad, route, moe_layer,  # noqa: F401
+                          grad_norm_clip)
