@@ -16,7 +16,7 @@ namespace ovl {
 // The head of the feed-forward calls' workspaces: the error record, then
 // int32 arrival counters, zero between calls.  Nothing else lies there, so
 // that calls of different kinds and sizes may use one workspace in turn.
-constexpr size_t kCounterBytes = 16384;
+constexpr size_t kCounterBytes = 65536;
 constexpr int32_t kCounters = (int32_t)(kCounterBytes - OVL_ERROR_RECORD_BYTES) / 4;
 
 constexpr uint64_t kDefaultSpinLimit = 1ull << 22;

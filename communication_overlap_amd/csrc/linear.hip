@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kLinMaxSplits = 16;
 
-// One product's tiles: items [item0, item0 + tiles_m * tiles_n * splits).
+// One product's tiles: tiles_m * tiles_n * splits items.
 struct LinJob {
   AnyOperand a, b;
   Epilogue epi;
@@ -33,7 +33,7 @@ struct LinJob {
   int32_t steps;      // K steps of 64
   int32_t split_steps;
   int32_t tiles_m, tiles_n, splits;
-  int32_t item0, items;
+  int32_t items;
 };
 
 // Column sums of dz, strips of 64 columns x ranges of rows.
@@ -44,22 +44,19 @@ struct LinSum {
   float* partial;  // [splits][n] when splits > 1
   int64_t ld, m, n, rows;  // rows of a range
   int32_t strips, splits;
-  int32_t item0, items;
+  int32_t items;
 };
 
 struct LinArgs {
   LinJob job[2];
   LinSum sum;
-  int32_t items;
+  int32_t second_first;  // job 1's tiles are the longer ones
 };
 
-// Item of workgroup b: consecutive items go to one die (workgroups are
-// handed to the dies in turn), so that a die's tiles share operand panels in
-// its L2.
-__device__ inline int lin_item(int b, int items) {
-  const int per = items / 8, extra = items % 8, x = b % 8, q = b / 8;
-  return x * per + min(x, extra) + q;
-}
+// Items of die x (workgroup b runs on die b % 8): a consecutive share, so that
+// a die's tiles share operand panels in its L2.
+__host__ __device__ inline int lin_share(int items, int x) { return items / 8 + (x < items % 8); }
+__device__ inline int lin_item(int items, int x, int q) { return x * (items / 8) + min(x, items % 8) + q; }
 
 template <class T>
 __device__ inline void lin_tile(const LinJob& j, int item, uint8_t* lds) {
@@ -145,19 +142,26 @@ __device__ inline void lin_sum(const LinSum& s, int item, uint8_t* lds) {
 template <class T>
 __global__ __launch_bounds__(64 * T::NW, T::NW == 4 ? 2 : 1) void lin_fwd_kernel(LinJob j) {
   extern __shared__ __align__(16) uint8_t lin_lds[];
-  lin_tile<T>(j, lin_item(blockIdx.x, j.items), lin_lds);
+  lin_tile<T>(j, lin_item(j.items, blockIdx.x % 8, blockIdx.x / 8), lin_lds);
 }
 
 template <class TA, class TB>
 __global__ __launch_bounds__(64 * TA::NW, TA::NW == 4 ? 2 : 1) void lin_grad_kernel(LinArgs a) {
   extern __shared__ __align__(16) uint8_t lin_lds[];
-  const int item = lin_item(blockIdx.x, a.items);
-  if (item < a.job[0].items)
-    lin_tile<TA>(a.job[0], item, lin_lds);
-  else if (item < a.job[0].items + a.job[1].items)
-    lin_tile<TB>(a.job[1], item - a.job[1].item0, lin_lds);
-  else
-    lin_sum<64 * TA::NW>(a.sum, item - a.sum.item0, lin_lds);
+  // Every die takes its share of each product and of the sums, the product
+  // with the longer tiles first (a die's last round is then short tiles and
+  // sums: 8192 x 4096 x 1792 ran in 405 us with the items of the one product
+  // all on the first dies).
+  const int x = blockIdx.x % 8;
+  int q = blockIdx.x / 8;
+  const int n0 = lin_share(a.job[0].items, x), n1 = lin_share(a.job[1].items, x);
+  if (a.second_first) q = q < n1 ? q + n0 : (q < n0 + n1 ? q - n1 : q);
+  if (q < n0)
+    lin_tile<TA>(a.job[0], lin_item(a.job[0].items, x, q), lin_lds);
+  else if (q < n0 + n1)
+    lin_tile<TB>(a.job[1], lin_item(a.job[1].items, x, q - n0), lin_lds);
+  else if (q - n0 - n1 < lin_share(a.sum.items, x))
+    lin_sum<64 * TA::NW>(a.sum, lin_item(a.sum.items, x, q - n0 - n1), lin_lds);
 }
 
 struct LinReduceArgs {
@@ -195,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinReduceArgs a) {
     }
 }
 
-// Few rows (decoding): column tiles of 64 x K ranges, rows.h's stream.  The
+// Few rows (decoding): column tiles of 128 x K ranges, rows.h's stream.  The
 // last range of a tile to arrive sums the ranges' partial products in range
 // order and applies the epilogue.
 struct LinRowArgs {
@@ -207,49 +211,62 @@ struct LinRowArgs {
   int32_t tiles, splits, steps, split_steps;
 };
 
+// One unit a workgroup.
+template <class C>
+struct LinRowGen {
+  const RowOperands* o;
+  const int32_t* rows;
+  int32_t s0, s1;
+  __device__ inline bool range(int32_t u, int32_t& a, int32_t& b) const {
+    a = s0;
+    b = s1;
+    return u == 0;
+  }
+  __device__ inline bool begin(int32_t u, RowLoads<C>& ld, int32_t& a, int32_t& b) const {
+    if (u == 0) ld.init(*o, rows);
+    return range(u, a, b);
+  }
+};
+
 template <class C>
 __global__ __launch_bounds__(kThreads) void lin_row_kernel(LinRowArgs a) {
   extern __shared__ __align__(16) uint8_t row_lds[];
   __shared__ int32_t rows[16 * C::NB];
   __shared__ int32_t flag;
+  constexpr int PR = C::COLS / 8;  // pieces of a row
   const int tile = blockIdx.x % a.tiles, sp = blockIdx.x / a.tiles;
   if (threadIdx.x < 16 * C::NB) rows[threadIdx.x] = (int)threadIdx.x < a.m ? (int)threadIdx.x : -1;
   __syncthreads();
   RowOperands o = a.o;
-  o.col0 = (int64_t)tile * kRowCols;
-  const int s0 = min(sp * a.split_steps, a.steps), s1 = min(s0 + a.split_steps, a.steps);
-  const float* st = row_product<C>(o, rows, s0, s1, row_lds);
-  const int pieces = (int)a.m * 8;
-  if (a.splits > 1) {
-    float* p = a.partial + (int64_t)sp * a.m * a.n;
+  o.col0 = (int64_t)tile * C::COLS;
+  const int s0 = min(sp * a.split_steps, a.steps);
+  LinRowGen<C> gen{&o, rows, s0, min(s0 + a.split_steps, a.steps)};
+  const int pieces = (int)a.m * PR;
+  row_stream<C>(gen, row_lds, [&](int32_t, const float* st) {
+    if (a.splits > 1) {
+      float* p = a.partial + (int64_t)sp * a.m * a.n;
+      for (int i = threadIdx.x; i < pieces; i += kThreads) {
+        const int row = i / PR;
+        const int64_t col = o.col0 + (i % PR) * 8;
+        if (col >= a.n) continue;
+        float v[8];
+        row_sums8<C>(v, st, 0, row, (i % PR) * 8);
+        store8_agent(v, p + row * a.n + col);
+      }
+      if (!row_arrive_last(a.counters + tile, a.splits, &flag)) return;
+    }
     for (int i = threadIdx.x; i < pieces; i += kThreads) {
-      const int row = i / 8;
-      const int64_t col = o.col0 + (i % 8) * 8;
+      const int row = i / PR;
+      const int64_t col = o.col0 + (i % PR) * 8;
       if (col >= a.n) continue;
       float v[8];
-      row_sums8<C>(v, st, 0, row, (i % 8) * 8);
-      store8_agent(v, p + row * a.n + col);
+      if (a.splits > 1)
+        row_ranges8(v, a.partial + row * a.n + col, a.splits, a.m * a.n);
+      else
+        row_sums8<C>(v, st, 0, row, (i % PR) * 8);
+      epilogue8(a.epi, row, col, v);
     }
-    if (!row_arrive_last(a.counters + tile, a.splits, &flag)) return;
-  }
-  for (int i = threadIdx.x; i < pieces; i += kThreads) {
-    const int row = i / 8;
-    const int64_t col = o.col0 + (i % 8) * 8;
-    if (col >= a.n) continue;
-    float v[8];
-    if (a.splits > 1) {
-      load8(v, a.partial, row * a.n + col, OVL_F32);
-      for (int s = 1; s < a.splits; ++s) {
-        float q[8];
-        load8(q, a.partial, ((int64_t)s * a.m + row) * a.n + col, OVL_F32);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] += q[c];
-      }
-    } else {
-      row_sums8<C>(v, st, 0, row, (i % 8) * 8);
-    }
-    epilogue8(a.epi, row, col, v);
-  }
+  });
 }
 
 // dz = bf16(dy * act'(z)), rows x cols with row strides.
@@ -349,16 +366,16 @@ ovl_status lin_fwd_launch(const LinArgs& a, hipStream_t stream) {
 
 template <class TA, class TB>
 ovl_status lin_grad_launch(LinArgs& a, hipStream_t stream) {
-  a.job[0].item0 = 0;
-  a.job[1].item0 = a.job[0].items;
-  a.sum.item0 = a.job[0].items + a.job[1].items;
-  a.items = a.sum.item0 + a.sum.items;
-  if (!a.items) return OVL_OK;
+  a.second_first = a.job[1].split_steps > a.job[0].split_steps;
+  int per = 0;
+  for (int x = 0; x < 8; ++x)
+    per = std::max(per, lin_share(a.job[0].items, x) + lin_share(a.job[1].items, x) + lin_share(a.sum.items, x));
+  if (!per) return OVL_OK;
   const void* fn = reinterpret_cast<const void*>(&lin_grad_kernel<TA, TB>);
   const int lds = std::max(TA::LDS_BYTES, TB::LDS_BYTES);
   ovl_status st = allow_lds(fn, lds);
   if (st) return st;
-  hipLaunchKernelGGL((lin_grad_kernel<TA, TB>), dim3(a.items), dim3(64 * TA::NW), lds, stream, a);
+  hipLaunchKernelGGL((lin_grad_kernel<TA, TB>), dim3(8 * per), dim3(64 * TA::NW), lds, stream, a);
   OVL_HIP_TRY(hipGetLastError());
   return lin_reduce(a, stream);
 }
@@ -431,6 +448,9 @@ ovl_status lin_grad_desc(gemm_epilogue_grad_desc* d) {
 // Few rows go to the streaming kernel (kLinRows, below).
 constexpr int64_t kLinRows = 32;
 
+using LinRow1 = RowCfg<false, false, 1, 1, 2, 36 * 1024>;
+using LinRow2 = RowCfg<false, false, 1, 2, 2, 36 * 1024>;
+
 struct LinRowShape {
   int32_t tiles, splits, steps, split_steps;
   size_t bytes;
@@ -438,9 +458,9 @@ struct LinRowShape {
 
 LinRowShape row_shape(const gemm_epilogue_desc& d) {
   LinRowShape s = {};
-  s.tiles = (int32_t)ceil_div(d.n, kRowCols);
+  s.tiles = (int32_t)ceil_div(d.n, LinRow1::COLS);
   s.steps = (int32_t)ceil_div(d.k, 32);
-  int64_t sp = std::min<int64_t>({kLinMaxSplits, ceil_div(3 * kLinCus, s.tiles), s.steps / 8});
+  int64_t sp = std::min<int64_t>({kLinMaxSplits, kLinCus / s.tiles, s.steps / 8});
   sp = std::max<int64_t>(sp, 1);
   s.split_steps = (int32_t)ceil_div(s.steps, sp);
   s.splits = (int32_t)ceil_div(s.steps, s.split_steps);
@@ -522,8 +542,7 @@ extern "C" ovl_status gemm_epilogue_run(const gemm_epilogue_desc* desc, const vo
     r.splits = rs.splits;
     r.steps = rs.steps;
     r.split_steps = rs.split_steps;
-    return d.m <= 16 ? row_launch<RowCfg<false, false, 1, 1>>(r, stream)
-                     : row_launch<RowCfg<false, false, 1, 2>>(r, stream);
+    return d.m <= 16 ? row_launch<LinRow1>(r, stream) : row_launch<LinRow2>(r, stream);
   }
   const LinShape s = fwd_shape(d);
   LinArgs args = {};

@@ -4,7 +4,7 @@
 // rows.h's streams, spread over the chip by (chosen expert, 64 columns,
 // range of k), and every reduction is done by whichever workgroup arrives
 // last, in a fixed order.
-//  1. Routing (with a router): ranges of hidden x groups of 16 tokens, sums
+//  1. Routing (with a router): ranges of hidden x groups of 4 tokens, sums
 //     in float64 so that a choice between two near logits does not hang on
 //     the order of a sum; the last range of a token group picks.
 //  2. Up: u = x w1, then h = act(gate) * up as bf16 planes (see ovl.h).
@@ -26,8 +26,10 @@ namespace {
 
 constexpr int kMoeTokens = 128, kMoeExperts = 256, kMoeTopk = 8;
 constexpr int kMoeRouteRows = 128;   // rows of the router a workgroup sums
-constexpr int kMoeRouteTokens = 16;  // tokens of a routing group
-constexpr int32_t kMoeDownCounters = 1024, kMoeRouteCounters = 16;  // then the up counters
+constexpr int kMoeRouteTokens = 4;   // tokens of a routing group (1 where there is one)
+// Arrival counters: down tiles, then (expert, up tile).
+constexpr int32_t kMoeDownCounters = 2048;
+constexpr int kMoeGroups = 256;  // workgroups of the experts' launches: one a compute unit
 
 struct MoeArgs {
   const uint16_t* x;
@@ -40,118 +42,130 @@ struct MoeArgs {
   const float* s2;
   void* out;
   uint16_t* h;      // [planes][pairs][inter]
-  float* up;        // [up_splits][pairs][n1] when up_splits > 1
-  float* down;      // [down_splits][pairs][hidden]
+  float* up;        // [up_max][pairs][n1] when up_max > 1
+  float* down;      // [down_max][pairs][hidden]
   double* logits;   // [chunks][tokens][experts]
   int32_t* down_counters;
-  int32_t* route_counters;
   int32_t* up_counters;
   int64_t hidden, inter, n1;
   int32_t tokens, experts, topk_n, pairs, act, out_type, norm_topk;
-  int32_t slots;  // a bound on the distinct experts chosen
-  int32_t up_tiles, up_splits, up_steps, up_split_steps;
-  int32_t down_tiles, down_splits, down_steps, down_split_steps;
+  int32_t up_tiles, up_max, up_steps;  // column tiles, most ranges of k, steps of k
+  int32_t down_tiles, down_max, down_steps;
   int32_t chunks;
+  int32_t fused;  // the down launch sums the choices itself
 };
 
 // ---------------------------------------------------------------- routing
 
-// a before b: the larger logit, NaN behind everything, then the lower id.
-__device__ inline bool moe_before(double a, int ia, double b, int ib) {
-  const bool na = isnan(a), nb = isnan(b);
-  if (na != nb) return nb;
-  if (!na && a != b) return a > b;
-  return ia < ib;
+// exp(x) of a float64 x, within two float32 steps: the hardware's exp2 of the
+// fraction, scaled (the device library's float64 exp is exact to the last
+// bits, and its code is long to fetch).
+__device__ inline float moe_exp(double x) {
+  const double y = x * 1.4426950408889634074;
+  if (y < -160.0) return 0.f;
+  const double n = rint(y);
+  return ldexpf(__builtin_amdgcn_exp2f((float)(y - n)), (int)n);
 }
 
-// Token t's choices, by one wavefront.
-__device__ inline void moe_pick(const MoeArgs& a, int t) {
+__device__ inline double moe_wave_max(double v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = fmax(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+// Token t's choices from its logits in LDS, by one wavefront: the largest
+// remaining one, topk times; among equals the lowest id, a NaN when nothing
+// else remains (fmax passes NaN over).
+__device__ inline void moe_pick(const MoeArgs& a, int t, const double* logits) {
   const int lane = lane_id();
   double v[4];
   bool have[4];
-  double top = -HUGE_VAL;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int e = lane + 64 * i;
-    have[i] = e < a.experts;
-    v[i] = 0;
-    if (have[i]) {
-      for (int c = 0; c < a.chunks; ++c) v[i] += a.logits[((int64_t)c * a.tokens + t) * a.experts + e];
-      top = fmax(top, v[i]);
-    }
+    have[i] = lane + 64 * i < a.experts;
+    v[i] = have[i] ? logits[lane + 64 * i] : 0.0;
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) top = fmax(top, __shfl_xor(top, d, 64));
-  double sum = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (have[i]) sum += exp(v[i] - top);
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-  double picked[kMoeTopk], chosen = 0;
-#pragma unroll
-  for (int j = 0; j < kMoeTopk; ++j) {
-    picked[j] = 0;
-    if (j >= a.topk_n) continue;
-    double b = 0;
-    int id = INT32_MAX;
+  double first = 0;  // the first choice's logit
+  float chosen = 0.f, mine = 0.f;
+  int my_id = 0;
+  for (int j = 0; j < a.topk_n; ++j) {
+    double m = -HUGE_VAL;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (have[i] && (id == INT32_MAX || moe_before(v[i], lane + 64 * i, b, id))) {
-        b = v[i];
-        id = lane + 64 * i;
-      }
+      if (have[i]) m = fmax(m, v[i]);
+    m = moe_wave_max(m);
+    int id = -1;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      const double ob = __shfl_xor(b, d, 64);
-      const int oi = __shfl_xor(id, d, 64);
-      if (oi != INT32_MAX && (id == INT32_MAX || moe_before(ob, oi, b, id))) {
-        b = ob;
-        id = oi;
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t eq = __ballot(have[i] && v[i] == m);
+      if (id < 0 && eq) id = 64 * i + __ffsll((unsigned long long)eq) - 1;
+    }
+    if (id < 0) {  // only NaN left
+      m = __builtin_nan("");
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t left = __ballot(have[i]);
+        if (id < 0 && left) id = 64 * i + __ffsll((unsigned long long)left) - 1;
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (lane + 64 * i == id) have[i] = false;
-    picked[j] = exp(b - top);
-    chosen += picked[j];
-    if (lane == 0) a.topk[t * a.topk_n + j] = id;
+    if (j == 0) first = m;
+    const float p = moe_exp(m - first);
+    chosen += p;
+    if (lane == j) {
+      mine = p;
+      my_id = id;
+    }
   }
-  const double den = a.norm_topk ? chosen : sum;
+  if (!a.norm_topk) {
+    chosen = 0.f;
 #pragma unroll
-  for (int j = 0; j < kMoeTopk; ++j)
-    if (j < a.topk_n && lane == 0) a.gates[t * a.topk_n + j] = (float)(picked[j] / den);
+    for (int i = 0; i < 4; ++i)
+      if (lane + 64 * i < a.experts) chosen += moe_exp(v[i] - first);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) chosen += __shfl_xor(chosen, d, 64);
+  }
+  if (lane < a.topk_n) {
+    a.topk[t * a.topk_n + lane] = my_id;
+    a.gates[t * a.topk_n + lane] = mine / chosen;
+  }
 }
 
-// Workgroup (range of hidden, 16 tokens): EP lanes across the experts, 256 /
-// EP rows of the router at a time, x from LDS.
-template <int EP>
-__global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeArgs a) {
-  constexpr int R = kThreads / EP;
-  __shared__ float xs[kMoeRouteTokens][kMoeRouteRows];
-  __shared__ double part[R][kMoeRouteTokens][EP];
-  __shared__ int32_t flag;
+// Workgroup (range of hidden, TT tokens): EP lanes across the experts, 256 /
+// EP rows of the router at a time, x from LDS; float64 sums of the range.
+template <int EP, int TT>
+__global__ __launch_bounds__(kThreads) void moe_logits_kernel(MoeArgs a) {
+  constexpr int R = kThreads / EP, U = 16;
+  __shared__ float xs[TT][kMoeRouteRows];
+  __shared__ double part[R][TT][EP];
   const int chunk = blockIdx.x % a.chunks, tg = blockIdx.x / a.chunks;
-  const int t0 = tg * kMoeRouteTokens, nt = min(kMoeRouteTokens, a.tokens - t0);
+  const int t0 = tg * TT, nt = min(TT, a.tokens - t0);
   const int64_t r0 = (int64_t)chunk * kMoeRouteRows;
   const int nr = (int)min((int64_t)kMoeRouteRows, a.hidden - r0);
-#pragma unroll
-  for (int j = 0; j < kMoeRouteTokens * kMoeRouteRows / kThreads; ++j) {
-    const int i = j * kThreads + threadIdx.x, t = i / kMoeRouteRows, r = i % kMoeRouteRows;
+  const int e = threadIdx.x % EP, rr = threadIdx.x / EP;
+  const uint16_t* w = a.router + r0 * a.experts + min(e, a.experts - 1);
+  for (int i = threadIdx.x; i < TT * kMoeRouteRows; i += kThreads) {
+    const int t = i / kMoeRouteRows, r = i % kMoeRouteRows;
     const float v = bf16_lo_f(a.x[(t0 + min(t, nt - 1)) * a.hidden + r0 + min(r, nr - 1)]);
     xs[t][r] = t < nt && r < nr ? v : 0.f;
   }
   __syncthreads();
-  const int e = threadIdx.x % EP, rr = threadIdx.x / EP;
-  double acc[kMoeRouteTokens] = {};
-  if (e < a.experts)
-    for (int r = rr; r < nr; r += R) {
-      const double w = bf16_lo_f(a.router[(r0 + r) * a.experts + e]);
+  double acc[TT] = {};
+  for (int r = rr; r < kMoeRouteRows; r += R * U) {
+    uint16_t q[U];
 #pragma unroll
-      for (int t = 0; t < kMoeRouteTokens; ++t) acc[t] += w * xs[t][r];
+    for (int u = 0; u < U; ++u) q[u] = w[(int64_t)min(r + u * R, nr - 1) * a.experts];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const double d = r + u * R < nr ? bf16_lo_f(q[u]) : 0.f;
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[t] += d * xs[t][min(r + u * R, kMoeRouteRows - 1)];
     }
+  }
 #pragma unroll
-  for (int t = 0; t < kMoeRouteTokens; ++t) part[rr][t][e] = acc[t];
+  for (int t = 0; t < TT; ++t) part[rr][t][e] = acc[t];
   __syncthreads();
   for (int i = threadIdx.x; i < nt * EP; i += kThreads) {
     const int t = i / EP, x = i % EP;
@@ -159,64 +173,198 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeArgs a) {
     double s = part[0][t][x];
 #pragma unroll
     for (int q = 1; q < R; ++q) s += part[q][t][x];
-    st8_agent(reinterpret_cast<uint64_t*>(a.logits + ((int64_t)chunk * a.tokens + t0 + t) * a.experts + x),
-              __builtin_bit_cast(uint64_t, s));
+    a.logits[((int64_t)chunk * a.tokens + t0 + t) * a.experts + x] = s;
   }
-  if (!row_arrive_last(a.route_counters + tg, a.chunks, &flag)) return;
-  for (int t = uniform(threadIdx.x >> 6); t < nt; t += kThreads / 64) moe_pick(a, t0 + t);
+}
+
+// One token a workgroup: the ranges' sums, 256 / EP threads a logit, those in
+// order, and the choice.
+template <int EP>
+__global__ __launch_bounds__(kThreads) void moe_pick_kernel(MoeArgs a) {
+  constexpr int R = kThreads / EP, U = 8;
+  __shared__ double part[R][EP];
+  const int t = blockIdx.x, e = threadIdx.x % EP, rr = threadIdx.x / EP;
+  const double* p = a.logits + (int64_t)t * a.experts + min(e, a.experts - 1);
+  const int64_t step = (int64_t)a.tokens * a.experts;
+  double s = 0;
+  for (int c = rr; c < a.chunks; c += R * U) {
+    double q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) q[u] = p[min(c + u * R, a.chunks - 1) * step];
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += c + u * R < a.chunks ? q[u] : 0.0;
+  }
+  part[rr][e] = s;
+  __syncthreads();
+  if (rr == 0) {
+#pragma unroll
+    for (int q = 1; q < R; ++q) s += part[q][e];
+    part[0][e] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) moe_pick(a, t, part[0]);
 }
 
 // ---------------------------------------------------------------- experts
 
-// The distinct experts among the chosen ids: returns the slot-th of them, in
-// ascending order (-1: fewer), and their number.
-__device__ inline int moe_expert(const MoeArgs& a, int slot, uint64_t* mask, int* active) {
-  if (threadIdx.x < 4) mask[threadIdx.x] = 0;
+// What a workgroup of the experts' launches knows of the routing.
+template <int N>  // rows of a unit
+struct MoeLds {
+  int32_t ids[kMoeTokens * kMoeTopk];
+  int32_t experts[kMoeExperts];  // the distinct experts chosen, ascending
+  uint64_t mask[4];
+  int32_t rows[2][kRowWaves][N];  // pairs of even and odd units, one table a wavefront
+  int32_t flag;
+};
+
+// (Shared memory reached through the generator is named as such: a generic
+// load counts as a global one, and a wait for it would empty the rings.)
+__device__ inline int32_t lds_word(const int32_t* p) { return *OVL_LDS(const int32_t, p); }
+
+// Reads the chosen ids and lists the distinct experts among them; returns how
+// many there are.
+template <int N>
+__device__ inline int moe_begin(const MoeArgs& a, MoeLds<N>& s) {
+  if (threadIdx.x < 4) s.mask[threadIdx.x] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < a.pairs; i += kThreads) {
     const int e = a.topk[i];
-    if (e >= 0 && e < a.experts)
-      atomicOr(reinterpret_cast<unsigned long long*>(&mask[e >> 6]), 1ull << (e & 63));
+    const bool here = e >= 0 && e < a.experts;
+    s.ids[i] = here ? e : -1;
+    if (here) atomicOr(reinterpret_cast<unsigned long long*>(&s.mask[e >> 6]), 1ull << (e & 63));
   }
   __syncthreads();
-  int n = 0, found = -1;
+  int n = 0, below = 0;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const uint64_t m = mask[w];
-    const int c = __popcll(m);
-    if (slot >= n && slot < n + c) {
-      uint64_t r = m;
-      for (int i = slot - n; i > 0; --i) r &= r - 1;
-      found = 64 * w + __ffsll((unsigned long long)r) - 1;
-    }
-    n += c;
+    const uint64_t m = s.mask[w];
+    if (w < (int)threadIdx.x >> 6) below += __popcll(m);
+    if (w == (int)threadIdx.x >> 6) below += __popcll(m & ((1ull << (threadIdx.x & 63)) - 1));
+    n += __popcll(m);
   }
-  *active = uniform(n);
-  return uniform(found);
+  static_assert(kThreads == kMoeExperts, "one thread an expert");
+  if (s.mask[threadIdx.x >> 6] >> (threadIdx.x & 63) & 1) s.experts[below] = threadIdx.x;
+  __syncthreads();
+  return uniform(n);
 }
 
-// Pairs first .. first + N - 1 of expert e, in order, into the LDS table
-// (-1 past the last); returns how many pairs e has.  By wavefront 0, between
-// barriers.
+// Pairs first .. first + N - 1 of expert e, in order, into this wavefront's
+// table (-1 past the last); returns how many pairs e has.
 template <int N>
-__device__ inline int moe_rows(const MoeArgs& a, int e, int first, int32_t* rows, int32_t* count) {
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const int lane = lane_id();
-    if (lane < N) rows[lane] = -1;
-    int n = 0;
-    for (int i = 0; i < a.pairs; i += 64) {
-      const bool hit = i + lane < a.pairs && a.topk[i + lane] == e;
-      const uint64_t m = __ballot(hit);
-      const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-      if (hit && at >= first && at < first + N) rows[at - first] = i + lane;
-      n += __popcll(m);
-    }
-    if (lane == 0) *count = n;
+__device__ inline int moe_rows(const MoeArgs& a, const int32_t* ids, int e, int first, int32_t* rows) {
+  const int lane = lane_id();
+  if (lane < N) *OVL_LDS(int32_t, rows + lane) = -1;
+  int n = 0;
+  for (int i = 0; i < a.pairs; i += 64) {
+    const bool hit = i + lane < a.pairs && lds_word(ids + min(i + lane, kMoeTokens * kMoeTopk - 1)) == e;
+    const uint64_t m = __ballot(hit);
+    const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+    if (hit && at >= first && at < first + N) *OVL_LDS(int32_t, rows + at - first) = i + lane;
+    n += __popcll(m);
   }
-  __syncthreads();
-  return uniform(*count);
+  return uniform(n);
 }
+
+// Ranges of k that a launch cuts its items into: as many as shorten its
+// rounds of kMoeGroups items, an item counting its steps and a fixed part
+// (about six steps of start and reduction; four more where the ranges' sums
+// meet in memory).  Lane l weighs l + 1 ranges.
+__device__ inline int moe_ranges(int items, int steps, int most) {
+  const int s = (int)lane_id() % 16 + 1;
+  const int per = (steps + s - 1) / s;
+  int cost = (items * s + kMoeGroups - 1) / kMoeGroups * (per + (s > 1 ? 10 : 6));
+  if (s > most || (s - 1) * per >= steps) cost = INT32_MAX;  // too many, or an empty range
+  int best = cost * 16 >= 0 && cost < INT32_MAX / 32 ? cost * 16 + s - 1 : INT32_MAX;
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) best = min(best, __shfl_xor(best, d, 64));
+  return uniform(best == INT32_MAX ? 1 : best % 16 + 1);
+}
+
+// The units of a workgroup: its items (expert, column tile, range of k) in
+// turn, each as often as the expert's rows fill a table.
+template <class C, bool UP>
+struct MoeGen {
+  static constexpr int N = C::ROWS;
+  const MoeArgs& a;
+  MoeLds<N>& s;
+  RowOperands o;
+  int32_t tiles, ranges, steps, per, items;
+  // The unit being loaded, and the unit being added up.
+  int32_t l_item, l_first, l_count, l_unit;
+  int32_t c_item, c_first, c_count, c_unit;
+
+  __device__ inline MoeGen(const MoeArgs& args, MoeLds<N>& lds, int active) : a(args), s(lds), o{} {
+    tiles = UP ? a.up_tiles : a.down_tiles;
+    steps = UP ? a.up_steps : a.down_steps;
+    ranges = moe_ranges(active * tiles, steps, UP ? a.up_max : a.down_max);
+    per = (steps + ranges - 1) / ranges;
+    items = active * tiles * ranges;
+    const int64_t rows = UP ? a.hidden : a.inter, cols = UP ? a.n1 : a.hidden;
+    o.w_bytes = rows * cols * (C::FP8 ? 1 : 2);
+    o.ldw = C::FP8 ? rows : cols;
+    o.cols = UP ? a.inter : a.hidden;
+    o.pair = a.inter;
+    o.x = UP ? a.x : a.h;
+    o.plane = UP ? 0 : a.pairs * a.inter;
+    o.x_bytes = UP ? a.tokens * a.hidden * 2 : C::PL * o.plane * 2;
+    o.ldx = rows;
+    o.k = rows;
+    l_item = c_item = blockIdx.x;
+    l_first = c_first = 0;
+    l_count = c_count = 0;
+    l_unit = c_unit = 0;
+  }
+  // Item = (expert * ranges + range) * tiles + tile.
+  __device__ inline int tile(int item) const { return item % tiles; }
+  __device__ inline int range_of(int item) const { return item / tiles % ranges; }
+  __device__ inline int slot(int item) const { return item / (tiles * ranges); }
+  __device__ inline void steps_of(int item, int32_t& s0, int32_t& s1) const {
+    s0 = min(range_of(item) * per, steps);
+    s1 = min(s0 + per, steps);
+  }
+  __device__ inline const int32_t* rows(int unit) const { return s.rows[unit & 1][threadIdx.x >> 6]; }
+
+  __device__ inline bool begin(int32_t u, RowLoads<C>& ld, int32_t& s0, int32_t& s1) {
+    if (u) {
+      l_first += N;
+      if (l_first >= l_count) {
+        l_first = 0;
+        l_item += gridDim.x;
+      }
+    }
+    if (l_item >= items) return false;
+    const int e = uniform(lds_word(s.experts + slot(l_item)));
+    int32_t* table = s.rows[u & 1][threadIdx.x >> 6];
+    l_count = moe_rows<N>(a, s.ids, e, l_first, table);
+    o.w = (UP ? a.w1 : a.w2) + e * o.w_bytes;
+    o.col0 = (int64_t)tile(l_item) * C::COLS;
+    ld.init(o, table, UP ? a.topk_n : 1);
+    steps_of(l_item, s0, s1);
+    return true;
+  }
+  __device__ inline bool range(int32_t u, int32_t& s0, int32_t& s1) {
+    if (u) {
+      c_first += N;
+      if (c_first >= c_count) {
+        c_first = 0;
+        c_item += gridDim.x;
+      }
+    }
+    if (c_item >= items) return false;
+    const int e = uniform(lds_word(s.experts + slot(c_item)));
+    // Only the count matters here: where the table holds every pair it is the
+    // table's own.
+    int n = 0;
+    for (int i = 0; i < a.pairs; i += 64)
+      n += __popcll(__ballot(i + lane_id() < a.pairs &&
+                             lds_word(s.ids + min(i + lane_id(), kMoeTokens * kMoeTopk - 1)) == e));
+    c_count = uniform(n);
+    c_unit = u;
+    steps_of(c_item, s0, s1);
+    return true;
+  }
+  __device__ inline bool last_of_item() const { return c_first + N >= c_count; }
+};
 
 // h as bf16 planes whose sum is h to 8 bits a plane.
 __device__ inline void moe_store_h(const MoeArgs& a, int planes, int pair, int64_t col, float (&h)[8]) {
@@ -253,187 +401,161 @@ __device__ inline void moe_scale(float (&v)[8], const float* s, int64_t i) {
 template <class C>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a, int planes) {
   extern __shared__ __align__(16) uint8_t moe_lds[];
-  __shared__ int32_t rows[16 * C::NB], toks[16 * C::NB];
-  __shared__ uint64_t mask[4];
-  __shared__ int32_t flag, count;
-  const int tile = blockIdx.x % a.up_tiles, sp = blockIdx.x / a.up_tiles % a.up_splits;
-  const int slot = blockIdx.x / (a.up_tiles * a.up_splits);
-  int active;
-  const int e = moe_expert(a, slot, mask, &active);
-  if (e < 0) return;
-  RowOperands o = {};
-  o.w_bytes = a.hidden * a.n1 * (C::FP8 ? 1 : 2);
-  o.w = a.w1 + e * o.w_bytes;
-  o.ldw = C::FP8 ? a.hidden : a.n1;
-  o.col0 = (int64_t)tile * kRowCols;
-  o.cols = a.inter;
-  o.pair = a.inter;
-  o.x = a.x;
-  o.x_bytes = a.tokens * a.hidden * 2;
-  o.ldx = a.hidden;
-  o.k = a.hidden;
-  const int s0 = min(sp * a.up_split_steps, a.up_steps), s1 = min(s0 + a.up_split_steps, a.up_steps);
-  int n = 1;
-  for (int first = 0; first < n; first += 16 * C::NB) {
-    n = moe_rows<16 * C::NB>(a, e, first, rows, &count);
-    if (threadIdx.x < 16 * C::NB) toks[threadIdx.x] = rows[threadIdx.x] < 0 ? -1 : rows[threadIdx.x] / a.topk_n;
-    __syncthreads();
-    const float* st = row_product<C>(o, toks, s0, s1, moe_lds);
-    for (int i = threadIdx.x; i < 16 * C::NB * 8; i += kThreads) {
-      const int pair = rows[i / 8];
-      const int64_t col = o.col0 + (i % 8) * 8;
+  __shared__ MoeLds<C::ROWS> s;
+  constexpr int PR = C::COLS / 8;  // pieces of a row
+  const int active = moe_begin(a, s);
+  MoeGen<C, true> gen(a, s, active);
+  row_stream<C>(gen, moe_lds, [&](int32_t u, const float* st) {
+    const int item = gen.c_item, sp = gen.range_of(item), tile = gen.tile(item);
+    const int e = uniform(lds_word(s.experts + gen.slot(item)));
+    const int64_t col0 = (int64_t)tile * C::COLS;
+    const int32_t* rows = gen.rows(u);
+    for (int i = threadIdx.x; i < C::PIECES; i += kThreads) {
+      const int pair = lds_word(rows + i / PR);
+      const int64_t col = col0 + (i % PR) * 8;
       if (pair < 0 || col >= a.inter) continue;
-      float g[8], u[8];
-      row_sums8<C>(g, st, 0, i / 8, (i % 8) * 8);
+      float g[8], v[8];
+      row_sums8<C>(g, st, 0, i / PR, (i % PR) * 8);
       moe_scale<C>(g, a.s1, e * a.n1 + col);
       if (C::PAIR) {
-        row_sums8<C>(u, st, C::WT - 1, i / 8, (i % 8) * 8);
-        moe_scale<C>(u, a.s1, e * a.n1 + a.inter + col);
+        row_sums8<C>(v, st, 1, i / PR, (i % PR) * 8);
+        moe_scale<C>(v, a.s1, e * a.n1 + a.inter + col);
       }
-      if (a.up_splits > 1) {
+      if (gen.ranges > 1) {
         float* p = a.up + ((int64_t)sp * a.pairs + pair) * a.n1 + col;
         store8_agent(g, p);
-        if (C::PAIR) store8_agent(u, p + a.inter);
+        if (C::PAIR) store8_agent(v, p + a.inter);
       } else {
-        moe_act<C>(a, planes, pair, col, g, u);
+        moe_act<C>(a, planes, pair, col, g, v);
       }
     }
-  }
-  if (a.up_splits == 1) return;
-  if (!row_arrive_last(a.up_counters + slot * a.up_tiles + tile, a.up_splits, &flag)) return;
-  for (int first = 0; first < n; first += 16 * C::NB) {
-    moe_rows<16 * C::NB>(a, e, first, rows, &count);
-    for (int i = threadIdx.x; i < 16 * C::NB * 8; i += kThreads) {
-      const int pair = rows[i / 8];
-      const int64_t col = o.col0 + (i % 8) * 8;
-      if (pair < 0 || col >= a.inter) continue;
-      float g[8] = {}, u[8] = {};
-      for (int s = 0; s < a.up_splits; ++s) {
-        float q[8];
-        const int64_t at = ((int64_t)s * a.pairs + pair) * a.n1 + col;
-        load8(q, a.up, at, OVL_F32);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) g[c] += q[c];
-        if (C::PAIR) {
-          load8(q, a.up, at + a.inter, OVL_F32);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) u[c] += q[c];
-        }
-      }
-      moe_act<C>(a, planes, pair, col, g, u);
+    if (gen.ranges == 1 || !gen.last_of_item()) return;
+    if (!row_arrive_last(a.up_counters + gen.slot(item) * gen.tiles + tile, gen.ranges, &s.flag)) return;
+    // All the expert's pairs, in the order of their ids.
+    for (int i = threadIdx.x; i < a.pairs * PR; i += kThreads) {
+      const int pair = i / PR;
+      const int64_t col = col0 + (i % PR) * 8;
+      if (lds_word(s.ids + pair) != e || col >= a.inter) continue;
+      float g[8], v[8];
+      const float* p = a.up + pair * a.n1 + col;
+      row_ranges8(g, p, gen.ranges, a.pairs * a.n1);
+      if (C::PAIR) row_ranges8(v, p + a.inter, gen.ranges, a.pairs * a.n1);
+      moe_act<C>(a, planes, pair, col, g, v);
     }
-  }
+  });
 }
 
-// out of one column tile: every token's choices in order.
-__device__ inline void moe_out(const MoeArgs& a, int64_t col0) {
-  for (int i = threadIdx.x; i < a.tokens * 8; i += kThreads) {
-    const int t = i / 8;
-    const int64_t col = col0 + (i % 8) * 8;
-    if (col >= a.hidden) continue;
-    float v[8] = {};
-    for (int j = 0; j < a.topk_n; ++j) {
-      const int pair = t * a.topk_n + j, e = a.topk[pair];
-      if (e < 0 || e >= a.experts) continue;
-      float y[8] = {};
-      for (int s = 0; s < a.down_splits; ++s) {
-        float q[8];
-        load8(q, a.down, ((int64_t)s * a.pairs + pair) * a.hidden + col, OVL_F32);
+// Eight columns of a token's output: its choices in order.
+__device__ inline void moe_out8(const MoeArgs& a, const int32_t* ids, int ranges, int t, int64_t col) {
+  float v[8] = {};
+  for (int j = 0; j < a.topk_n; ++j) {
+    const int pair = t * a.topk_n + j;
+    if (lds_word(ids + pair) < 0) continue;
+    float y[8];
+    row_ranges8(y, a.down + pair * a.hidden + col, ranges, a.pairs * a.hidden);
+    const float g = a.gates[pair];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) y[c] += q[c];
-      }
-      const float g = a.gates[pair];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] += g * y[c];
-    }
-    store8(v, a.out, t * a.hidden + col, a.out_type);
+    for (int c = 0; c < 8; ++c) v[c] += g * y[c];
   }
+  store8(v, a.out, t * a.hidden + col, a.out_type);
+}
+
+// out of one column tile.
+template <int PR>
+__device__ inline void moe_out(const MoeArgs& a, const int32_t* ids, int ranges, int64_t col0) {
+  for (int i = threadIdx.x; i < a.tokens * PR; i += kThreads)
+    if (col0 + (i % PR) * 8 < a.hidden) moe_out8(a, ids, ranges, i / PR, col0 + (i % PR) * 8);
 }
 
 template <class C>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
   extern __shared__ __align__(16) uint8_t moe_lds[];
-  __shared__ int32_t rows[16 * C::NB];
-  __shared__ uint64_t mask[4];
-  __shared__ int32_t flag, count;
-  const int tile = blockIdx.x % a.down_tiles, sp = blockIdx.x / a.down_tiles % a.down_splits;
-  const int slot = blockIdx.x / (a.down_tiles * a.down_splits);
-  int active;
-  const int e = moe_expert(a, slot, mask, &active);
-  if (active == 0 && slot == 0 && sp == 0) moe_out(a, (int64_t)tile * kRowCols);  // zeros
-  if (e < 0) return;
-  RowOperands o = {};
-  o.w_bytes = a.hidden * a.inter * (C::FP8 ? 1 : 2);
-  o.w = a.w2 + e * o.w_bytes;
-  o.ldw = C::FP8 ? a.inter : a.hidden;
-  o.col0 = (int64_t)tile * kRowCols;
-  o.cols = a.hidden;
-  o.x = a.h;
-  o.plane = a.pairs * a.inter;
-  o.x_bytes = C::PL * o.plane * 2;
-  o.ldx = a.inter;
-  o.k = a.inter;
-  const int s0 = min(sp * a.down_split_steps, a.down_steps), s1 = min(s0 + a.down_split_steps, a.down_steps);
-  int n = 1;
-  for (int first = 0; first < n; first += 16 * C::NB) {
-    n = moe_rows<16 * C::NB>(a, e, first, rows, &count);
-    const float* st = row_product<C>(o, rows, s0, s1, moe_lds);
-    for (int i = threadIdx.x; i < 16 * C::NB * 8; i += kThreads) {
-      const int pair = rows[i / 8];
-      const int64_t col = o.col0 + (i % 8) * 8;
+  __shared__ MoeLds<C::ROWS> s;
+  constexpr int PR = C::COLS / 8;
+  const int active = moe_begin(a, s);
+  if (active == 0 && a.fused)  // no expert of this rank: zeros
+    for (int t = blockIdx.x; t < a.down_tiles; t += gridDim.x) moe_out<PR>(a, s.ids, 1, (int64_t)t * C::COLS);
+  MoeGen<C, false> gen(a, s, active);
+  row_stream<C>(gen, moe_lds, [&](int32_t u, const float* st) {
+    const int item = gen.c_item, sp = gen.range_of(item), tile = gen.tile(item);
+    const int e = uniform(lds_word(s.experts + gen.slot(item)));
+    const int64_t col0 = (int64_t)tile * C::COLS;
+    const int32_t* rows = gen.rows(u);
+    for (int i = threadIdx.x; i < C::PIECES; i += kThreads) {
+      const int pair = lds_word(rows + i / PR);
+      const int64_t col = col0 + (i % PR) * 8;
       if (pair < 0 || col >= a.hidden) continue;
       float v[8];
-      row_sums8<C>(v, st, 0, i / 8, (i % 8) * 8);
+      row_sums8<C>(v, st, 0, i / PR, (i % PR) * 8);
       moe_scale<C>(v, a.s2, e * a.hidden + col);
-      store8_agent(v, a.down + ((int64_t)sp * a.pairs + pair) * a.hidden + col);
+      float* p = a.down + ((int64_t)sp * a.pairs + pair) * a.hidden + col;
+      if (a.fused)
+        store8_agent(v, p);
+      else
+        store8(v, p, 0, OVL_F32);
     }
-  }
-  if (row_arrive_last(a.down_counters + tile, active * a.down_splits, &flag)) moe_out(a, o.col0);
+    if (a.fused && gen.last_of_item() && row_arrive_last(a.down_counters + tile, active * gen.ranges, &s.flag))
+      moe_out<PR>(a, s.ids, gen.ranges, col0);
+  });
+}
+
+// The sum on its own, where the down launch has many units a workgroup and an
+// arrival after each would hold up its stream.
+template <class C>
+__global__ __launch_bounds__(kThreads) void moe_sum_kernel(MoeArgs a) {
+  __shared__ MoeLds<C::ROWS> s;
+  const int active = moe_begin(a, s);
+  const int ranges = moe_ranges(active * a.down_tiles, a.down_steps, a.down_max);
+  const int per = (int)(a.hidden / 8);
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.tokens * per; i += gridDim.x * kThreads)
+    moe_out8(a, s.ids, ranges, i / per, (int64_t)(i % per) * 8);
 }
 
 // ---------------------------------------------------------------- host
 
 struct MoeShape {
-  int32_t slots, pairs, planes, chunks, groups;
-  int32_t up_tiles, up_splits, up_steps, up_split_steps;
-  int32_t down_tiles, down_splits, down_steps, down_split_steps;
+  int32_t pairs, planes, chunks;
+  bool few;  // few tokens an expert
+  int32_t up_tiles, up_max, up_steps;
+  int32_t down_tiles, down_max, down_steps;
   size_t h_off, up_off, down_off, logits_off, bytes;
 };
 
-constexpr int kMoeTarget = 512;  // workgroups that fill the chip
+// A wavefront's ring: what the staged sums and the tables leave of LDS.
+constexpr int kMoeRing = 34 * 1024;
+constexpr int64_t kMoePartial = 64 << 20;  // bytes that the ranges of k may take
 
-void moe_split(int64_t k, int ks, int64_t items, int max_splits, int32_t* steps, int32_t* splits, int32_t* per) {
-  *steps = (int32_t)ceil_div(k, ks);
-  int64_t sp = std::min<int64_t>({(int64_t)max_splits, ceil_div(kMoeTarget, items), *steps / 8});
-  sp = std::max<int64_t>(sp, 1);
-  *per = (int32_t)ceil_div(*steps, sp);
-  *splits = (int32_t)ceil_div(*steps, *per);
+// Most ranges of k: 16, at least 4 steps each, within the partial products'
+// room and the counters.
+int32_t moe_most(int32_t steps, int64_t floats, bool counted) {
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({counted ? 16 : 1, steps / 4, kMoePartial / (floats * 4)}));
 }
 
 MoeShape moe_shape(const moe_layer_desc& d) {
   MoeShape s = {};
-  const int ks = d.w_type == OVL_FP8 ? 64 : 32;
+  const bool fp8 = d.w_type == OVL_FP8;
+  const int ks = fp8 ? 128 : 32;
   s.pairs = (int32_t)(d.tokens * d.topk);
-  s.slots = std::max(1, std::min(d.experts, s.pairs));
   s.planes = d.out_type == OVL_F32 ? 3 : 2;
   s.chunks = (int32_t)ceil_div(d.hidden, kMoeRouteRows);
-  s.groups = (int32_t)ceil_div(d.tokens, kMoeRouteTokens);
-  s.up_tiles = (int32_t)ceil_div(d.inter, kRowCols);
-  s.down_tiles = (int32_t)ceil_div(d.hidden, kRowCols);
-  const int64_t up_items = (int64_t)s.slots * s.up_tiles;
-  const bool up_counted = up_items <= kCounters - kMoeDownCounters - kMoeRouteCounters;
-  moe_split(d.hidden, ks, up_items, up_counted ? 16 : 1, &s.up_steps, &s.up_splits, &s.up_split_steps);
-  moe_split(d.inter, ks, (int64_t)s.slots * s.down_tiles, 16, &s.down_steps, &s.down_splits, &s.down_split_steps);
-  const int64_t n1 = d.gated ? 2 * d.inter : d.inter;
+  s.few = 2 * s.pairs <= 3 * d.experts;
+  s.up_tiles = (int32_t)ceil_div(d.inter, fp8 && d.gated ? 32 : 64);
+  s.down_tiles = (int32_t)ceil_div(d.hidden, fp8 ? 64 : 128);
+  s.up_steps = (int32_t)ceil_div(d.hidden, ks);
+  s.down_steps = (int32_t)ceil_div(d.inter, ks);
+  const int64_t n1 = d.gated ? 2 * d.inter : d.inter, pairs = std::max(s.pairs, 1);
+  const int64_t up_items = std::min<int64_t>(d.experts, pairs) * s.up_tiles;
+  s.up_max = moe_most(s.up_steps, pairs * n1, up_items <= kCounters - kMoeDownCounters);
+  s.down_max = moe_most(s.down_steps, pairs * d.hidden, true);
   size_t off = kCounterBytes;
   const auto take = [&](int64_t bytes) {
     const size_t at = off;
     off += aligned_up((size_t)bytes, 256);
     return at;
   };
-  s.h_off = take((int64_t)s.planes * s.pairs * d.inter * 2);
-  s.up_off = take(s.up_splits > 1 ? (int64_t)s.up_splits * s.pairs * n1 * 4 : 0);
-  s.down_off = take((int64_t)s.down_splits * s.pairs * d.hidden * 4);
+  s.h_off = take(s.planes * pairs * d.inter * 2);
+  s.up_off = take(s.up_max > 1 ? s.up_max * pairs * n1 * 4 : 0);
+  s.down_off = take(s.down_max * pairs * d.hidden * 4);
   s.logits_off = take((int64_t)s.chunks * d.tokens * d.experts * 8);
   s.bytes = off;
   return s;
@@ -459,8 +581,7 @@ template <class C>
 ovl_status moe_up(const MoeArgs& a, int planes, hipStream_t stream) {
   ovl_status st = allow_lds(reinterpret_cast<const void*>(&moe_up_kernel<C>), C::LDS);
   if (st) return st;
-  hipLaunchKernelGGL((moe_up_kernel<C>), dim3(a.slots * a.up_tiles * a.up_splits), dim3(kThreads), C::LDS, stream, a,
-                     planes);
+  hipLaunchKernelGGL((moe_up_kernel<C>), dim3(kMoeGroups), dim3(kThreads), C::LDS, stream, a, planes);
   OVL_HIP_TRY(hipGetLastError());
   return OVL_OK;
 }
@@ -469,25 +590,54 @@ template <class C>
 ovl_status moe_down(const MoeArgs& a, hipStream_t stream) {
   ovl_status st = allow_lds(reinterpret_cast<const void*>(&moe_down_kernel<C>), C::LDS);
   if (st) return st;
-  hipLaunchKernelGGL((moe_down_kernel<C>), dim3(a.slots * a.down_tiles * a.down_splits), dim3(kThreads), C::LDS,
-                     stream, a);
+  hipLaunchKernelGGL((moe_down_kernel<C>), dim3(kMoeGroups), dim3(kThreads), C::LDS, stream, a);
   OVL_HIP_TRY(hipGetLastError());
+  if (!a.fused) {
+    hipLaunchKernelGGL((moe_sum_kernel<C>), dim3(ceil_div(a.tokens * a.hidden / 8, kThreads)), dim3(kThreads), 0, stream,
+                       a);
+    OVL_HIP_TRY(hipGetLastError());
+  }
   return OVL_OK;
 }
 
 template <int EP>
-ovl_status moe_route(const MoeArgs& a, int groups, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_route_kernel<EP>), dim3(a.chunks * groups), dim3(kThreads), 0, stream, a);
+ovl_status moe_route(const MoeArgs& a, hipStream_t stream) {
+  if (a.tokens == 1)
+    hipLaunchKernelGGL((moe_logits_kernel<EP, 1>), dim3(a.chunks), dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((moe_logits_kernel<EP, kMoeRouteTokens>), dim3(a.chunks * ceil_div(a.tokens, kMoeRouteTokens)),
+                       dim3(kThreads), 0, stream, a);
+  OVL_HIP_TRY(hipGetLastError());
+  hipLaunchKernelGGL((moe_pick_kernel<EP>), dim3(a.tokens), dim3(kThreads), 0, stream, a);
   OVL_HIP_TRY(hipGetLastError());
   return OVL_OK;
 }
 
-template <bool FP8, int NB>
-ovl_status moe_experts(const MoeArgs& a, bool gated, int planes, hipStream_t stream) {
-  const ovl_status st = gated ? moe_up<RowCfg<FP8, true, 1, NB>>(a, planes, stream)
-                              : moe_up<RowCfg<FP8, false, 1, NB>>(a, planes, stream);
+// bf16 weights: NB blocks of 16 rows a unit.
+template <int NB>
+ovl_status moe_bf16(const MoeArgs& a, bool gated, int planes, hipStream_t stream) {
+  const ovl_status st = gated ? moe_up<RowCfg<false, true, 1, NB, 1, kMoeRing>>(a, planes, stream)
+                              : moe_up<RowCfg<false, false, 1, NB, 1, kMoeRing>>(a, planes, stream);
   if (st) return st;
-  return planes == 2 ? moe_down<RowCfg<FP8, false, 2, NB>>(a, stream) : moe_down<RowCfg<FP8, false, 3, NB>>(a, stream);
+  return planes == 2 ? moe_down<RowCfg<false, false, 2, NB, 2, kMoeRing>>(a, stream)
+                     : moe_down<RowCfg<false, false, 3, NB, 2, kMoeRing>>(a, stream);
+}
+
+// Codes: a step's rows take as much LDS as its weights, so that few rows leave
+// a deeper ring: 4 a unit where an expert has few tokens, else what fits.
+ovl_status moe_fp8(const MoeArgs& a, bool gated, int planes, bool few, hipStream_t stream) {
+  if (few) {
+    const ovl_status st = gated ? moe_up<RowCfg<true, true, 1, 1, 1, kMoeRing, 4>>(a, planes, stream)
+                                : moe_up<RowCfg<true, false, 1, 1, 2, kMoeRing, 4>>(a, planes, stream);
+    if (st) return st;
+    return planes == 2 ? moe_down<RowCfg<true, false, 2, 1, 2, kMoeRing, 4>>(a, stream)
+                       : moe_down<RowCfg<true, false, 3, 1, 2, kMoeRing, 4>>(a, stream);
+  }
+  const ovl_status st = gated ? moe_up<RowCfg<true, true, 1, 2, 1, kMoeRing>>(a, planes, stream)
+                              : moe_up<RowCfg<true, false, 1, 2, 2, kMoeRing>>(a, planes, stream);
+  if (st) return st;
+  return planes == 2 ? moe_down<RowCfg<true, false, 2, 1, 2, kMoeRing>>(a, stream)
+                     : moe_down<RowCfg<true, false, 3, 1, 2, kMoeRing, 8>>(a, stream);
 }
 
 }  // namespace
@@ -533,8 +683,7 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
   a.down = reinterpret_cast<float*>(ws + s.down_off);
   a.logits = reinterpret_cast<double*>(ws + s.logits_off);
   a.down_counters = reinterpret_cast<int32_t*>(ws + OVL_ERROR_RECORD_BYTES);
-  a.route_counters = a.down_counters + kMoeDownCounters;
-  a.up_counters = a.route_counters + kMoeRouteCounters;
+  a.up_counters = a.down_counters + kMoeDownCounters;
   a.hidden = d->hidden;
   a.inter = d->inter;
   a.n1 = d->gated ? 2 * d->inter : d->inter;
@@ -545,26 +694,19 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
   a.act = d->act;
   a.out_type = d->out_type;
   a.norm_topk = d->norm_topk;
-  a.slots = s.slots;
   a.up_tiles = s.up_tiles;
-  a.up_splits = s.up_splits;
+  a.up_max = s.up_max;
   a.up_steps = s.up_steps;
-  a.up_split_steps = s.up_split_steps;
   a.down_tiles = s.down_tiles;
-  a.down_splits = s.down_splits;
+  a.down_max = s.down_max;
   a.down_steps = s.down_steps;
-  a.down_split_steps = s.down_split_steps;
   a.chunks = s.chunks;
+  a.fused = (int64_t)s.pairs * s.down_tiles <= kMoeGroups;  // at most one unit a workgroup
   if (router) {
-    st = d->experts <= 64 ? moe_route<64>(a, s.groups, stream)
-                          : (d->experts <= 128 ? moe_route<128>(a, s.groups, stream)
-                                               : moe_route<256>(a, s.groups, stream));
+    st = d->experts <= 64 ? moe_route<64>(a, stream)
+                          : (d->experts <= 128 ? moe_route<128>(a, stream) : moe_route<256>(a, stream));
     if (st) return st;
   }
-  // Groups of 32 rows only where more than 16 tokens can meet at an expert.
-  if (fp8)
-    return d->tokens <= 16 ? moe_experts<true, 1>(a, d->gated, s.planes, stream)
-                           : moe_experts<true, 2>(a, d->gated, s.planes, stream);
-  return d->tokens <= 16 ? moe_experts<false, 1>(a, d->gated, s.planes, stream)
-                         : moe_experts<false, 2>(a, d->gated, s.planes, stream);
+  if (fp8) return moe_fp8(a, d->gated, s.planes, s.few, stream);
+  return d->tokens <= 16 ? moe_bf16<1>(a, d->gated, s.planes, stream) : moe_bf16<2>(a, d->gated, s.planes, stream);
 }

@@ -1,6 +1,6 @@
 // A few rows times a streamed weight: y[r][c] = sum_k x[r][k] w[k][c] for at
-// most 16 * NB rows, 64 columns (PAIR: and 64 more, `pair` columns further
-// on) and a range of k, by one workgroup of four wavefronts.
+// most ROWS rows, COLS columns (PAIR: and as many more, `pair` columns
+// further on) and a range of k, by one workgroup of four wavefronts.
 //
 // Every weight is read once and used for few rows, so the bound is HBM: what
 // counts is bytes in flight.  The wavefronts split the range of k and share
@@ -12,10 +12,13 @@
 // the vector units out of the loop:
 //   bf16 weights [k][n]: steps of 32 k; LDS rows of 64 columns, fragments by
 //     the transposing read ds_read_b64_tr_b16;
-//   E4M3 weights [n][k]: steps of 64 k; LDS rows of 64 codes, 16 codes a
-//     lane, widened to bf16 (exact) in front of the matrix instruction.  A
-//     lane group's 16 codes serve two instructions of 8 k each; the rows'
-//     fragments take the same k.
+//   E4M3 weights [n][k]: steps of 128 k; LDS rows of 128 codes, 32 columns,
+//     widened to bf16 (exact) in front of the matrix instruction.  A lane
+//     reads 16 codes at a time, which serve two instructions of 8 k each; the
+//     rows' fragments take the same k.
+// Either way every row of the weight is read in whole 128-byte lines by one
+// instruction: with steps of 64 codes, half a line each, the experts' launch
+// streamed at 4.1 TB/s, with the next step's half just behind it.
 // PL: x comes as that many bf16 planes whose sum is the value, each
 // multiplied on its own (a float32 h as 2 or 3 planes: 16 or 24 bits).
 // LDS rows are XOR-permuted in 16-byte chunks, as in gemm_core.h.
@@ -27,23 +30,34 @@
 namespace ovl {
 
 constexpr int kRowWaves = 4;
-constexpr int kRowCols = 64;
-
-template <bool FP8_, bool PAIR_, int PL_, int NB_>
+// AD: tiles of TC columns side by side.  XR: rows of x that a step holds, 16
+// or, for codes, 4 or 8 (the matrix instruction's other columns then repeat
+// them, and are not looked at).  RING: LDS bytes of a
+// wavefront's ring.
+template <bool FP8_, bool PAIR_, int PL_, int NB_, int AD_, int RING, int XR_ = 16>
 struct RowCfg {
   static constexpr bool FP8 = FP8_, PAIR = PAIR_;
-  static constexpr int PL = PL_, NB = NB_;
-  static constexpr int KS = FP8 ? 64 : 32;             // k of a step
-  static constexpr int WT = PAIR ? 2 : 1;              // weight tiles of a step
-  static constexpr int XB = 16 * KS * 2;               // bytes of a step's 16 rows
-  static constexpr int XQ = XB / 1024;                 // load instructions of them
+  static constexpr int PL = PL_, NB = NB_, AD = AD_;
+  static constexpr int XR = XR_;
+  static constexpr int ROWS = XR == 16 ? 16 * NB : XR;  // rows of a unit
+  static constexpr int TC = FP8 ? 32 : 64;             // columns of a tile
+  static constexpr int COLS = TC * AD;                 // columns of a workgroup (PAIR: of either half)
+  static constexpr int PIECES = ROWS * COLS / 8;       // 8-column pieces of its rows
+  static constexpr int KS = FP8 ? 128 : 32;            // k of a step
+  static constexpr int WT = PAIR ? 2 * AD : AD;        // weight tiles of a step
+  static constexpr int BLOCKS = WT * TC / 16;          // 16-column blocks of a step
+  static constexpr int XB = XR * KS * 2;               // bytes of a step's block of rows
+  static constexpr int XQ = XB / 1024;                 // load instructions of it
   static constexpr int LPS = 4 * WT + XQ * PL * NB;    // load instructions of a step
   static constexpr int STEP = LPS * 1024;
-  static constexpr int D = 20 * 1024 / STEP >= 2 ? 20 * 1024 / STEP : 2;  // steps in the ring
+  static_assert(XB % 1024 == 0 && (XR == 16 || (XR <= 8 && NB == 1)), "whole load instructions");
+  static_assert(BLOCKS % kRowWaves == 0, "the blocks divide over the waves");
+  static constexpr int D = RING / STEP >= 2 ? RING / STEP : 2;  // steps in the ring
   static constexpr int WAVE_LDS = D * STEP;
-  static constexpr int SUMS = kRowWaves * WT * 16 * NB * (kRowCols + 4) * 4;  // the waves' sums, staged over the rings
-  static constexpr int LDS = kRowWaves * WAVE_LDS > SUMS ? kRowWaves * WAVE_LDS : SUMS;
+  static constexpr int PITCH = TC + 4;                 // floats of a staged row
+  static constexpr int LDS = kRowWaves * WAVE_LDS + WT * 16 * NB * PITCH * 4;  // the rings, then the staged sums
   static_assert((D - 1) * LPS <= 63, "the load counter holds 63 loads");
+  static_assert(D * STEP <= RING, "the ring holds two steps");
 };
 
 struct RowOperands {
@@ -63,51 +77,55 @@ struct RowOperands {
 template <class C>
 struct RowLoads {
   u32x4 sw[C::WT], sx;
-  uint32_t w_off[4];            // this lane's offsets at k = 0, or kOOB
+  uint32_t w_off[C::AD][4];     // this lane's offsets at k = 0, or kOOB
   uint32_t w_k;                 // FP8: the lane's first k in a step
   uint32_t x_off[C::NB * C::XQ];
   uint32_t x_k[C::XQ];
   uint32_t w_step, plane_b;
   int32_t k;
 
-  // rows: LDS table of 16 * NB row numbers, -1 for none.
-  __device__ inline void init(const RowOperands& o, const int32_t* rows) {
+  // rows: LDS table of ROWS numbers, -1 for none; number / div is the row.
+  __device__ inline void init(const RowOperands& o, const int32_t* rows, int32_t div = 1) {
     const uint32_t l = lane_id();
     k = (int32_t)o.k;
     plane_b = (uint32_t)(o.plane * 2);
     sx = make_srd(o.x, o.x_bytes);
 #pragma unroll
     for (int t = 0; t < C::WT; ++t) {
-      const int64_t c = o.col0 + t * o.pair;
+      const int64_t c = o.col0 + t / C::AD * o.pair + t % C::AD * C::TC;
       const int64_t skip = C::FP8 ? c * o.ldw : c * 2;
       sw[t] = make_srd(static_cast<const uint8_t*>(o.w) + skip, o.w_bytes - skip);
     }
     if constexpr (C::FP8) {
       w_step = C::KS;
-      w_k = ((l & 3) ^ ((l >> 3) & 3)) * 16;  // row l/4 of an instruction's 16; chunk (l%4) ^ (row/2 % 4)
+      w_k = ((l & 7) ^ (l >> 3)) * 16;  // row l/8 of an instruction's 8; chunk (l%8) ^ (row % 8)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t row = q * 16 + l / 4;
-        w_off[q] = o.col0 + row < o.cols ? (uint32_t)(row * o.ldw) + w_k : kOOB;
-      }
+      for (int t = 0; t < C::AD; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t row = q * 8 + l / 8;
+          w_off[t][q] = o.col0 + t * C::TC + row < o.cols ? (uint32_t)(row * o.ldw) + w_k : kOOB;
+        }
     } else {
       w_step = (uint32_t)(C::KS * o.ldw * 2);
       w_k = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t row = q * 8 + l / 8, c = (l & 7) ^ swz_w(row);
-        w_off[q] = o.col0 + c * 8 < o.cols ? row * (uint32_t)(o.ldw * 2) + c * 16 : kOOB;
-      }
+      for (int t = 0; t < C::AD; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t row = q * 8 + l / 8, c = (l & 7) ^ swz_w(row);
+          w_off[t][q] = o.col0 + t * C::TC + c * 8 < o.cols ? row * (uint32_t)(o.ldw * 2) + c * 16 : kOOB;
+        }
     }
 #pragma unroll
     for (int q = 0; q < C::XQ; ++q) {
-      const uint32_t row = C::FP8 ? q * 8 + l / 8 : l / 4;
-      const uint32_t c = C::FP8 ? (l & 7) ^ (row & 7) : (l & 3) ^ ((row >> 1) & 3);
+      const uint32_t row = C::FP8 ? q * 4 + l / 16 : l / 4;
+      const uint32_t c = C::FP8 ? (l & 15) ^ (row & 15) : (l & 3) ^ ((row >> 1) & 3);
       x_k[q] = c * 8;
 #pragma unroll
       for (int b = 0; b < C::NB; ++b) {
-        const int32_t r = rows[b * 16 + row];
-        x_off[b * C::XQ + q] = r >= 0 ? (uint32_t)(r * o.ldx * 2) + c * 16 : kOOB;
+        const int32_t r = *OVL_LDS(const int32_t, rows + b * 16 + row);
+        x_off[b * C::XQ + q] = r >= 0 ? (uint32_t)(r / div * o.ldx * 2) + c * 16 : kOOB;
       }
     }
   }
@@ -120,7 +138,7 @@ struct RowLoads {
     for (int t = 0; t < C::WT; ++t)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        uint32_t o = w_off[q] + (uint32_t)(k0 / C::KS) * w_step;
+        uint32_t o = w_off[t % C::AD][q] + (uint32_t)(k0 / C::KS) * w_step;
         if constexpr (C::FP8) o = k0 + (int32_t)w_k < k ? o : kOOB;
         load_to_lds(sw[t], slot + (t * 4 + q) * 1024, o);
       }
@@ -136,24 +154,17 @@ struct RowLoads {
 
 template <class C>
 struct RowAcc {
-  f32x4 v[C::WT][4][C::NB];  // [tile][16 columns][16 rows]: lane l holds row l%16, columns 4*(l/16) ..+3
+  f32x4 v[C::BLOCKS][C::NB];  // [16 columns][16 rows]: lane l holds row l%16, columns 4*(l/16) ..+3
 };
 
-// Eight E4M3 codes (two words) widened to bf16.
+// Eight E4M3 codes (two words) widened to bf16, which holds them exactly.
 __device__ inline bf16x8 fp8_to_bf16(uint32_t a, uint32_t b) {
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  bf16x8 r;
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const uint32_t c = w ? b : a;
-    const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);
-    const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
-    r[4 * w] = (__bf16)lo[0];
-    r[4 * w + 1] = (__bf16)lo[1];
-    r[4 * w + 2] = (__bf16)hi[0];
-    r[4 * w + 3] = (__bf16)hi[1];
-  }
-  return r;
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false);
+  const bf16x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
+  const bf16x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false);
+  const bf16x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
+  return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
 template <class C>
@@ -161,29 +172,35 @@ __device__ inline void row_step(RowAcc<C>& acc, const uint8_t* slot) {
   const uint32_t l = lane_id(), g = l >> 4, r = l & 15;
   const uint8_t* xs = slot + C::WT * 4096;
   if constexpr (C::FP8) {
-    bf16x8 x[C::PL][C::NB][2];
+    const uint32_t xr = r % C::XR;
 #pragma unroll
-    for (int p = 0; p < C::PL; ++p)
+    for (int h = 0; h < 2; ++h) {  // 64 codes at a time: lane group g holds k = 64 h + 16 g ..+15
+      bf16x8 x[C::PL][C::NB][2];
 #pragma unroll
-      for (int b = 0; b < C::NB; ++b)
+      for (int p = 0; p < C::PL; ++p)
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          x[p][b][s] = *OVL_LDS(const bf16x8, xs + (p * C::NB + b) * C::XB + r * 128 + (((2 * g + s) ^ (r & 7)) * 16));
+        for (int b = 0; b < C::NB; ++b)
 #pragma unroll
-    for (int t = 0; t < C::WT; ++t)
+          for (int s = 0; s < 2; ++s)
+            x[p][b][s] = *OVL_LDS(const bf16x8, xs + (p * C::NB + b) * C::XB + xr * 256 +
+                                                    (((8 * h + 2 * g + s) ^ xr) * 16));
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) {
-        const uint32_t row = cb * 16 + r;
-        const u32x4 q = *OVL_LDS(const u32x4, slot + t * 4096 + row * 64 + ((g ^ ((row >> 1) & 3)) * 16));
-        const bf16x8 w0 = fp8_to_bf16(q[0], q[1]), w1 = fp8_to_bf16(q[2], q[3]);
+      for (int t = 0; t < C::WT; ++t)
 #pragma unroll
-        for (int p = 0; p < C::PL; ++p)
+        for (int cb = 0; cb < 2; ++cb) {
+          const uint32_t row = cb * 16 + r;
+          const u32x4 q = *OVL_LDS(const u32x4, slot + t * 4096 + row * 128 + (((4 * h + g) ^ (row & 7)) * 16));
+          const bf16x8 w0 = fp8_to_bf16(q[0], q[1]), w1 = fp8_to_bf16(q[2], q[3]);
 #pragma unroll
-          for (int b = 0; b < C::NB; ++b) {
-            acc.v[t][cb][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, x[p][b][0], acc.v[t][cb][b], 0, 0, 0);
-            acc.v[t][cb][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, x[p][b][1], acc.v[t][cb][b], 0, 0, 0);
-          }
-      }
+          for (int p = 0; p < C::PL; ++p)
+#pragma unroll
+            for (int b = 0; b < C::NB; ++b) {
+              f32x4& v = acc.v[t * 2 + cb][b];
+              v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, x[p][b][0], v, 0, 0, 0);
+              v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, x[p][b][1], v, 0, 0, 0);
+            }
+        }
+    }
   } else {
     bf16x8 x[C::PL][C::NB];
 #pragma unroll
@@ -205,7 +222,7 @@ __device__ inline void row_step(RowAcc<C>& acc, const uint8_t* slot) {
         for (int q = 0; q < C::PL; ++q)
 #pragma unroll
           for (int b = 0; b < C::NB; ++b)
-            acc.v[t][cb][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[q][b], acc.v[t][cb][b], 0, 0, 0);
+            acc.v[t * 4 + cb][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[q][b], acc.v[t * 4 + cb][b], 0, 0, 0);
       }
   }
 }
@@ -224,69 +241,99 @@ __device__ inline void row_wait(int steps) {
   }
 }
 
-// The sums over steps [s0, s1) of KS, all four wavefronts' together, staged
-// in LDS: sums[tile][row][64 + 4], in every thread's sight when it returns.
-// Every sum is made of the waves' in wave order, each in k order.  `rows` is
-// an LDS table outside the ring; the ring must be free.
-template <class C>
-__device__ inline const float* row_product(const RowOperands& o, const int32_t* rows, int32_t s0, int32_t s1,
-                                           uint8_t* lds) {
+// Streams the workgroup's units one after the other, a unit being one set of
+// rows x columns x range of k.  The loads run ahead of the products by the
+// ring's depth, across the end of a unit: while one unit's sums are added up
+// and stored, the next one's weights are on their way.
+//   gen.begin(u, ld, s0, s1): sets up the loads of unit u and its range of
+//     steps; false when there is no such unit.  No global loads in it: it runs
+//     inside the product loop, where a wait would empty the ring.
+//     It is called at most one unit ahead of done().
+//   gen.range(u, s0, s1): the range alone.
+//   done(u, sums): unit u's sums of all four wavefronts, staged in LDS as
+//     sums[tile][row][TC + 4], in every thread's sight.
+// Every sum is made of the waves' in an order fixed by its columns, each
+// wave's in k order.
+template <class C, class Gen, class Done>
+__device__ inline void row_stream(Gen& gen, uint8_t* lds, Done done) {
   const int wave = uniform((int)(threadIdx.x >> 6));
-  RowAcc<C> acc;
-#pragma unroll
-  for (int t = 0; t < C::WT; ++t)
-#pragma unroll
-    for (int cb = 0; cb < 4; ++cb)
-#pragma unroll
-      for (int b = 0; b < C::NB; ++b) acc.v[t][cb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // The waves take steps in turn, so that the workgroup reads its range front
+  // to back.
+  const auto steps_of = [&](int32_t s0, int32_t s1) {
+    return max(0, s1 - s0 - wave + kRowWaves - 1) / kRowWaves;
+  };
   RowLoads<C> ld;
-  ld.init(o, rows);
-  const int32_t per = (s1 - s0 + kRowWaves - 1) / kRowWaves;
-  const int32_t b = min(s0 + wave * per, s1), n = min(b + per, s1) - b;
-  uint8_t* ring = lds + wave * C::WAVE_LDS;
+  const uint8_t* ring = lds + wave * C::WAVE_LDS;
   const uint32_t ring_a = lds_addr(ring);
+  float* st = reinterpret_cast<float*>(lds + kRowWaves * C::WAVE_LDS);
+  // The unit being loaded, its next step and how many this wave has of it.
+  int32_t lu = 0, li = 0, ln = 0, l0 = 0, l1 = 0;
+  bool more = gen.begin(0, ld, l0, l1);
+  if (more) ln = steps_of(l0, l1);
+  int32_t islot = 0, uslot = 0, ahead = 0;  // ahead: steps issued and not yet used
+  int32_t u = 0;                            // the unit being added up
+  const auto issue_next = [&]() {
+    while (more && li == ln && lu <= u) {   // at most one unit ahead
+      more = gen.begin(++lu, ld, l0, l1);
+      li = 0;
+      ln = more ? steps_of(l0, l1) : 0;
+    }
+    if (!more || li == ln) return;
+    ld.issue(ring_a + islot * C::STEP, (l0 + wave + li * kRowWaves) * C::KS);
+    islot = islot + 1 == C::D ? 0 : islot + 1;
+    ++li;
+    ++ahead;
+  };
   wave_drain();
-  for (int32_t i = 0; i < C::D - 1 && i < n; ++i) ld.issue(ring_a + i * C::STEP, (b + i) * C::KS);
-  row_wait<C::LPS, C::D - 2>(max(0, min(C::D - 2, n - 1)));
-  int32_t slot = 0;
-  for (int32_t i = 0; i < n; ++i) {
-    const int32_t nxt = i + C::D - 1;
-    const int32_t nslot = slot ? slot - 1 : C::D - 1;
-    if (nxt < n) ld.issue(ring_a + nslot * C::STEP, (b + nxt) * C::KS);
-    row_step<C>(acc, ring + slot * C::STEP);
-    row_wait<C::LPS, C::D - 2>(max(0, min(nxt, n - 1) - (i + 1)));
-    slot = slot + 1 == C::D ? 0 : slot + 1;
-  }
-  wave_drain();
-  __syncthreads();  // every wave's ring is done with
-  constexpr int P = kRowCols + 4, TILE = 16 * C::NB * P, ALL = C::WT * TILE;
-  float* st = reinterpret_cast<float*>(lds);
-  {
+  int32_t s0, s1;
+  for (; gen.range(u, s0, s1); ++u) {
+    // Fill the ring and have the first step there; then every step of the
+    // loop refills the slot used last and waits for the next one.
+    for (int i = ahead; i < C::D - 1; ++i) issue_next();
+    row_wait<C::LPS, C::D - 2>(min(C::D - 2, max(0, ahead - 1)));
+    RowAcc<C> acc;
+#pragma unroll
+    for (int k = 0; k < C::BLOCKS; ++k)
+#pragma unroll
+      for (int b = 0; b < C::NB; ++b) acc.v[k][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int32_t n = steps_of(s0, s1);
+    for (int32_t i = 0; i < n; ++i) {
+      issue_next();
+      row_step<C>(acc, ring + uslot * C::STEP);
+      uslot = uslot + 1 == C::D ? 0 : uslot + 1;
+      --ahead;
+      row_wait<C::LPS, C::D - 2>(max(0, ahead - 1));
+    }
+    // Four rounds: in round r wave w puts in (round 0) or adds its blocks k
+    // with k = w + r mod 4.
+    __syncthreads();  // the staged sums of the unit before are done with
     const uint32_t l = lane_id();
 #pragma unroll
-    for (int t = 0; t < C::WT; ++t)
+    for (int r = 0; r < kRowWaves; ++r) {
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb)
+      for (int k = 0; k < C::BLOCKS; ++k)
+        if (((k - r) & 3) == wave) {
+          constexpr int PB = C::TC / 16;  // blocks of a tile
 #pragma unroll
-        for (int nb = 0; nb < C::NB; ++nb)
-          *OVL_LDS(f32x4, st + wave * ALL + t * TILE + (nb * 16 + (l & 15)) * P + cb * 16 + 4 * (l >> 4)) =
-              acc.v[t][cb][nb];
+          for (int b = 0; b < C::NB; ++b) {
+            float* p = st + (k / PB * 16 * C::NB + b * 16 + (l & 15)) * C::PITCH + k % PB * 16 + 4 * (l >> 4);
+            f32x4 v = acc.v[k][b];
+            if (r) v += *OVL_LDS(const f32x4, p);
+            *OVL_LDS(f32x4, p) = v;
+          }
+        }
+      __syncthreads();
+    }
+    done(u, st);
+    wave_drain();  // done's loads are known to have landed: no wait for them inside the product loop
   }
-  __syncthreads();
-  for (int i = threadIdx.x * 4; i < ALL; i += kThreads * 4) {
-    f32x4 v = *OVL_LDS(const f32x4, st + i);
-#pragma unroll
-    for (int w = 1; w < kRowWaves; ++w) v += *OVL_LDS(const f32x4, st + w * ALL + i);
-    *OVL_LDS(f32x4, st + i) = v;
-  }
-  __syncthreads();
-  return st;
 }
 
-// Eight sums of a staged tile.
+// Eight sums of a staged row, from column col (a multiple of 8) of half
+// `half` (PAIR: 0 or 1).
 template <class C>
-__device__ inline void row_sums8(float (&v)[8], const float* st, int tile, int row, int col) {
-  const float* p = st + (tile * 16 * C::NB + row) * (kRowCols + 4) + col;
+__device__ inline void row_sums8(float (&v)[8], const float* st, int half, int row, int col) {
+  const float* p = st + ((half * C::AD + col / C::TC) * 16 * C::NB + row) * C::PITCH + col % C::TC;
   const f32x4 a = *OVL_LDS(const f32x4, p), b = *OVL_LDS(const f32x4, p + 4);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -302,6 +349,30 @@ __device__ inline void store8_agent(const float (&v)[8], float* p) {
   for (int c = 0; c < 4; ++c)
     st8_agent(reinterpret_cast<uint64_t*>(p) + c,
               (uint64_t)__builtin_bit_cast(uint32_t, v[2 * c]) | (uint64_t)__builtin_bit_cast(uint32_t, v[2 * c + 1]) << 32);
+}
+
+// Eight sums of `ranges` partial products, `stride` floats apart, added in
+// range order; four ranges' loads go out together.
+__device__ inline void row_ranges8(float (&v)[8], const float* p, int ranges, int64_t stride) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] = 0.f;
+  for (int s = 0; s < ranges; s += 4) {
+    f32x4 q[4][2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const f32x4* r = reinterpret_cast<const f32x4*>(p + min(s + u, ranges - 1) * stride);
+      q[u][0] = r[0];
+      q[u][1] = r[1];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (s + u < ranges)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[c] += q[u][0][c];
+          v[4 + c] += q[u][1][c];
+        }
+  }
 }
 
 // Arrival at a counter of `expected` workgroups: true, in every thread, for
