@@ -185,7 +185,7 @@ __device__ inline double gc_sum_range(const GcArgs& a, int64_t v0, int64_t v1) {
 
 __device__ inline void gc_scale_slot(const GcTensor& g, int64_t i, u32x4 v, float coef, bool vec) {
   if (vec) {
-    reinterpret_cast<u32x4*>(g.dst - g.head)[i] = gc_scaled(v, g.f32, coef);
+    __builtin_nontemporal_store(gc_scaled(v, g.f32, coef), reinterpret_cast<u32x4*>(g.dst - g.head) + i);
     return;
   }
   // dst lies differently within its 16 bytes than src: element by element.
@@ -201,7 +201,10 @@ __device__ inline void gc_scale_slot(const GcTensor& g, int64_t i, u32x4 v, floa
   }
 }
 
-// dst = src * coef over slots [v0, v1), from the last to the first.
+// dst = src * coef over slots [v0, v1), from the last to the first.  Both
+// streams are nontemporal, so that the stores do not push what the first pass
+// left in the caches out before it is read again (1 GiB of gradients, both
+// launches: 590 -> 553 us; 32 MiB: 19.2 -> 18.1).
 __device__ inline void gc_scale_range(const GcArgs& a, int64_t v0, int64_t v1, float coef) {
   if (v0 >= v1) return;
   const int lane = lane_id();
@@ -222,7 +225,7 @@ __device__ inline void gc_scale_range(const GcArgs& a, int64_t v0, int64_t v1, f
     for (; i - (kGcU - 1) * 64 >= w0; i -= kGcU * 64) {
       u32x4 v[kGcU];
 #pragma unroll
-      for (int u = 0; u < kGcU; ++u) v[u] = p[i - u * 64];
+      for (int u = 0; u < kGcU; ++u) v[u] = __builtin_nontemporal_load(p + i - u * 64);
 #pragma unroll
       for (int u = 0; u < kGcU; ++u) gc_scale_slot(g, i - u * 64, v[u], coef, vec);
     }
@@ -393,7 +396,7 @@ extern "C" ovl_status grad_norm_clip_run(grad_clip_plan_t p, float max_norm, flo
     return OVL_OK;
   }
   const int64_t groups =
-      std::min<int64_t>({kGcMaxGroups, (int64_t)di.cus * 8, ceil_div(a.slots, 64 * kGcU * (kThreads / 64))});
+      std::min<int64_t>({kGcMaxGroups, (int64_t)di.cus * 4, ceil_div(a.slots, 64 * kGcU * (kThreads / 64))});
   a.per_wave = ceil_div(a.slots, groups * (kThreads / 64));
   hipLaunchKernelGGL(gc_norm_kernel, dim3((uint32_t)groups), dim3(kThreads), 0, stream, a);
   OVL_HIP_TRY(hipGetLastError());

@@ -135,28 +135,73 @@ struct Epilogue {
   int32_t out_type, res_type, act;
 };
 
-__device__ inline void epilogue8(const Epilogue& e, int64_t row, int64_t col, float (&v)[8]) {
-  if (e.bias) {
-    float b[8];
-    load8(b, e.bias, col, OVL_F32);
+// What the epilogue of a piece reads beside the sums, as it lies in memory:
+// eight elements of the residual or of z_in (a call has one of them at most).
+struct EpilogueIn {
+  u32x4 q[2];
+};
+
+__device__ inline void unpack8(float (&v)[8], const EpilogueIn& x, int type) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] += b[c];
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t a = x.q[0][c], b = x.q[1][c];
+    if (type == OVL_F32) {
+      v[c] = __builtin_bit_cast(float, a);
+      v[4 + c] = __builtin_bit_cast(float, b);
+    } else {
+      v[2 * c] = bf16_lo_f(a);
+      v[2 * c + 1] = bf16_hi_f(a);
+    }
   }
+}
+
+__device__ inline EpilogueIn epilogue_load(const Epilogue& e, int64_t row, int64_t col) {
+  EpilogueIn x = {};
+  if (e.residual && e.res_type == OVL_F32) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(e.residual) + row * e.ld_res + col);
+    x.q[0] = p[0];
+    x.q[1] = p[1];
+  } else if (e.residual) {
+    x.q[0] = ld16(static_cast<const uint16_t*>(e.residual) + row * e.ld_res + col);
+  } else if (e.z_in) {
+    x.q[0] = ld16(static_cast<const uint16_t*>(e.z_in) + row * e.ld_z + col);
+  }
+  return x;
+}
+
+// Eight columns' bias, or zeros.
+__device__ inline void epilogue_bias(float (&b)[8], const Epilogue& e, int64_t col, bool there) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) b[c] = 0.f;
+  if (e.bias && there) load8(b, e.bias, col, OVL_F32);
+}
+
+__device__ inline void epilogue8(const Epilogue& e, int64_t row, int64_t col, float (&v)[8], const float (&bias)[8],
+                                 const EpilogueIn& x) {
+  if (e.bias)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] += bias[c];
   if (e.z_out) store8(v, e.z_out, row * e.ld_z + col, OVL_BF16);
   if (e.z_in) {
     float z[8];
-    load8(z, e.z_in, row * e.ld_z + col, OVL_BF16);
+    unpack8(z, x, OVL_BF16);
     act_grad8(v, z, e.act);
   } else {
     act8(v, e.act);
   }
   if (e.residual) {
     float r[8];
-    load8(r, e.residual, row * e.ld_res + col, e.res_type);
+    unpack8(r, x, e.res_type);
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] += r[c];
   }
   store8(v, e.out, row * e.ld_out + col, e.out_type);
+}
+
+__device__ inline void epilogue8(const Epilogue& e, int64_t row, int64_t col, float (&v)[8]) {
+  float b[8];
+  epilogue_bias(b, e, col, true);
+  epilogue8(e, row, col, v, b, epilogue_load(e, row, col));
 }
 
 }  // namespace ovl

@@ -6,8 +6,11 @@
 //   grad     dB = A^T dZ      both K-strided ([m][k], [m][n]: contraction over m).
 // One workgroup of NW = 4 or 8 wavefronts computes a BM x BN tile in 32 x 32
 // blocks (v_mfma_f32_32x32x16_bf16), the waves forming a 2 x (NW/2) grid.  K
-// advances in steps of 64 through two LDS stages filled by buffer loads that
-// write LDS directly.
+// advances in steps of 64 through NS LDS stages filled NS - 1 steps ahead by
+// buffer loads that write LDS directly: two stages of 64 KiB for 256 x 256
+// tiles, which keep the matrix units busy over a step, and up to four of
+// 32 KiB for 128 x 128 tiles alone on their compute unit, where a step is
+// shorter than a load takes.
 //   K-contiguous operand: LDS [row][64 k], 128 bytes a row; a fragment is one
 //   ds_read_b128 (8 consecutive k of one row).
 //   K-strided operand: LDS [k][rows], a fragment is two ds_read_b64_tr_b16
@@ -131,16 +134,17 @@ __device__ inline void any_read(AnyFragData* d, const uint8_t* area, const AnyFr
   }
 }
 
-template <int BM_, int BN_, int NW_, bool AKC_, bool BKC_>
+template <int BM_, int BN_, int NW_, bool AKC_, bool BKC_, int NS_ = 2>
 struct AnyTile {
-  static constexpr int BM = BM_, BN = BN_, NW = NW_;
+  static constexpr int BM = BM_, BN = BN_, NW = NW_, NS = NS_;
   static constexpr bool AKC = AKC_, BKC = BKC_;
   static constexpr int WN = NW / 2;
   static constexpr int FM = BM / 64, FN = BN / (32 * WN);
   using SA = AnySide<BM, NW, AKC>;
   using SB = AnySide<BN, NW, BKC>;
   static constexpr int STAGE = SA::BYTES + SB::BYTES;
-  static constexpr int LDS_BYTES = 2 * STAGE;
+  static constexpr int LPS = SA::Q + SB::Q;  // load instructions per wave per stage
+  static constexpr int LDS_BYTES = NS * STAGE;
   static constexpr int READS = SB::PIECES * FN + SA::PIECES * FM;  // LDS reads of one sub-step
   struct Acc {
     f32x16 v[FM][FN];
@@ -239,45 +243,65 @@ __device__ inline void any_tile(typename T::Acc& acc, const AnyOperand& a, const
   lp.fa.init((wave / T::WN) * (T::BM / 2));
   lp.fb.init((wave % T::WN) * (T::BN / T::WN));
   const uint32_t base = lds_addr(lds);
-  if (s0 < s1) {
-    lp.template issue_a<0, T::SA::Q>(base, s0);
-    lp.template issue_b<0, T::SB::Q>(base, s0);
-  }
+  constexpr int NS = T::NS;
+  const int32_t steps = s1 - s0;
   wave_drain();
+  for (int32_t i = 0; i < NS - 1 && i < steps; ++i) {
+    lp.template issue_a<0, T::SA::Q>(base + i * T::STAGE, s0 + i);
+    lp.template issue_b<0, T::SB::Q>(base + i * T::STAGE, s0 + i);
+  }
+  wait_stage_loads<T::LPS, NS - 2>(max(0, min(NS - 2, steps - 1)));
   __syncthreads();
-  for (int32_t s = s0; s < s1; ++s) {
-    const uint32_t cur = (uint32_t)(s - s0) & 1;
+  int32_t cur = 0;
+  for (int32_t s = 0; s < steps; ++s) {
     const uint8_t* stage = lds + cur * T::STAGE;
-    const uint32_t nst = base + (cur ^ 1) * T::STAGE;
-    const bool load = s + 1 < s1;
+    const uint32_t nst = base + (cur ? cur - 1 : NS - 1) * T::STAGE;  // the stage of step s - 1, filled for s + NS - 1
+    const int32_t nxt = s + NS - 1;
+    const bool load = nxt < steps;
     typename T::Frags f0, f1;
     lp.template read<0, T::READS>(f0, stage, 0);
     OVL_SCHED_FENCE();
-    lp.template groups<0, T::FM>(acc, f0, f1, stage, nst, s + 1, load);
-    lp.template groups<T::FM, T::FM>(acc, f1, f0, stage, nst, s + 1, load);
-    lp.template groups<2 * T::FM, T::FM>(acc, f0, f1, stage, nst, s + 1, load);
-    lp.template groups<3 * T::FM, T::FM>(acc, f1, f0, stage, nst, s + 1, load);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lp.template groups<0, T::FM>(acc, f0, f1, stage, nst, s0 + nxt, load);
+    lp.template groups<T::FM, T::FM>(acc, f1, f0, stage, nst, s0 + nxt, load);
+    lp.template groups<2 * T::FM, T::FM>(acc, f0, f1, stage, nst, s0 + nxt, load);
+    lp.template groups<3 * T::FM, T::FM>(acc, f1, f0, stage, nst, s0 + nxt, load);
+    wait_stage_loads<T::LPS, NS - 2>(max(0, min(nxt, steps - 1) - (s + 1)));
     __syncthreads();
+    cur = cur + 1 == NS ? 0 : cur + 1;
   }
 }
 
 // The tile through LDS, a wave's own part at a time, so that rows leave in
-// 8-column pieces: f(row, col, v[8]) for every piece of the wave's sub-tile,
-// row/col relative to the tile.  The area must be free (any_tile's end) and
-// holds 32 rows of a wave's columns for each wave.
-template <class T, class F>
-__device__ inline void any_rows(const typename T::Acc& acc, uint8_t* lds, F f) {
+// 8-column pieces: f(row, col, v[8], x) for every piece of the wave's
+// sub-tile, row/col relative to the tile (a lane's col is the same for all its
+// pieces); x = load(row, col), what the epilogue reads beside the sums, is
+// fetched for a block of 32 rows at once (one piece at a time, each waiting
+// for its own load, 1000 x 2056 x 520 with a float32 residual took 17.4 us
+// instead of 12).  The area must be free (any_tile's end) and holds 32 rows
+// of a wave's columns for each wave.
+template <class T>
+__device__ inline int any_col() {  // the column of this lane's pieces
+  constexpr int COLS = T::BN / T::WN;
+  return uniform((int)(threadIdx.x >> 6)) % T::WN * COLS + lane_id() % (COLS / 8) * 8;
+}
+
+template <class T, class L, class F>
+__device__ inline void any_rows(const typename T::Acc& acc, uint8_t* lds, L load, F f) {
   constexpr int COLS = T::BN / T::WN;           // a wave's columns: 64
   constexpr int PITCH = COLS + 4;               // floats of a staged row (the pad spreads the banks)
   constexpr int LPR = COLS / 8, RPI = 64 / LPR;  // lanes per row, rows per read
+  constexpr int N = 32 / RPI;                   // pieces of a lane in a block
   static_assert(T::NW * 32 * PITCH * 4 <= T::LDS_BYTES, "the staged rows fit the stages");
   const int lane = lane_id();
   const int wave = uniform((int)(threadIdx.x >> 6));
   float* area = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
-  const int wm = (wave / T::WN) * (T::BM / 2), wn = (wave % T::WN) * COLS;
+  const int wm = (wave / T::WN) * (T::BM / 2), col = lane % LPR * 8, tcol = any_col<T>();
 #pragma unroll
   for (int fm = 0; fm < T::FM; ++fm) {
+    const int row0 = wm + fm * 32 + lane / LPR;
+    decltype(load(0, 0)) x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = load(row0 + i * RPI, tcol);
 #pragma unroll
     for (int fn = 0; fn < T::FN; ++fn)
 #pragma unroll
@@ -285,8 +309,8 @@ __device__ inline void any_rows(const typename T::Acc& acc, uint8_t* lds, F f) {
         *OVL_LDS(float, area + ((r & 3) + 8 * (r >> 2) + 4 * (lane >> 5)) * PITCH + fn * 32 + (lane & 31)) =
             acc.v[fm][fn][r];
 #pragma unroll 1
-    for (int i = 0; i < 32 / RPI; ++i) {
-      const int row = i * RPI + lane / LPR, col = (lane % LPR) * 8;
+    for (int i = 0; i < N; ++i) {
+      const int row = i * RPI + lane / LPR;
       float v[8];
       const f32x4 lo = *OVL_LDS(const f32x4, area + row * PITCH + col);
       const f32x4 hi = *OVL_LDS(const f32x4, area + row * PITCH + col + 4);
@@ -295,7 +319,11 @@ __device__ inline void any_rows(const typename T::Acc& acc, uint8_t* lds, F f) {
         v[c] = lo[c];
         v[4 + c] = hi[c];
       }
-      f(wm + fm * 32 + row, wn + col, v);
+      f(wm + fm * 32 + row, tcol, v, x[0]);
+      // The next piece's turn (moving the registers keeps the loop's body, with
+      // every activation in it, from being laid out N times).
+#pragma unroll
+      for (int j = 0; j + 1 < N; ++j) x[j] = x[j + 1];
     }
   }
 }

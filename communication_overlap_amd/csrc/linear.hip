@@ -73,13 +73,20 @@ __device__ inline void lin_tile(const LinJob& j, int item, uint8_t* lds) {
   any_tile<T>(acc, j.a, j.b, m0, n0, s0, s1, lds);
   if (j.splits > 1) {
     float* p = j.partial + (int64_t)sp * j.m * j.n;
-    any_rows<T>(acc, lds, [&](int row, int col, float (&v)[8]) {
+    any_rows<T>(acc, lds, [](int, int) { return 0; }, [&](int row, int col, float (&v)[8], int) {
       if (m0 + row < j.m && n0 + col < j.n) store8(v, p, (m0 + row) * j.n + n0 + col, OVL_F32);
     });
   } else {
-    any_rows<T>(acc, lds, [&](int row, int col, float (&v)[8]) {
-      if (m0 + row < j.m && n0 + col < j.n) epilogue8(j.epi, m0 + row, n0 + col, v);
-    });
+    const auto there = [&](int row, int col) { return m0 + row < j.m && n0 + col < j.n; };
+    float bias[8];
+    epilogue_bias(bias, j.epi, n0 + any_col<T>(), there(0, any_col<T>()));
+    any_rows<T>(acc, lds,
+                [&](int row, int col) {
+                  return there(row, col) ? epilogue_load(j.epi, m0 + row, n0 + col) : EpilogueIn{};
+                },
+                [&](int row, int col, float (&v)[8], const EpilogueIn& x) {
+                  if (there(row, col)) epilogue8(j.epi, m0 + row, n0 + col, v, bias, x);
+                });
   }
 }
 
@@ -296,11 +303,16 @@ using Da256 = AnyTile<256, 256, 8, true, true>;
 using Da128 = AnyTile<128, 128, 4, true, true>;
 using Db256 = AnyTile<256, 256, 8, false, false>;
 using Db128 = AnyTile<128, 128, 4, false, false>;
+// The same, four stages deep: one workgroup a compute unit.
+using Fwd128D = AnyTile<128, 128, 4, true, false, 4>;
+using Da128D = AnyTile<128, 128, 4, true, true, 4>;
+using Db128D = AnyTile<128, 128, 4, false, false, 4>;
 
 // Tile edge and K splits of the products of one launch.  Both the size
 // queries and the launches use this.
 struct LinShape {
   int tile;
+  bool deep;  // 128 x 128 tiles, at most one item a compute unit
   int32_t splits[2];
   int32_t sum_splits;
   size_t partial_off[2], sum_off, bytes;
@@ -308,22 +320,39 @@ struct LinShape {
 
 constexpr int kLinCus = 256;  // the plan is made for a whole MI355X, so that sizes do not hang on the device
 
+// What a second launch costs, in K steps of a 128 x 128 tile (about 6 us of
+// 0.4): below that many saved, a tile is not cut.
+constexpr int64_t kLinSplitSteps = 16;
+
 LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum_n) {
   LinShape s = {};
-  int64_t t256 = 0, t128 = 0;
+  int64_t t256 = 0, t128 = 0, steps[2] = {1, 1}, tiles[2] = {}, longest = 1;
   for (int j = 0; j < jobs; ++j) {
     t256 += ceil_div(mnk[j][0], 256) * ceil_div(mnk[j][1], 256);
-    t128 += ceil_div(mnk[j][0], 128) * ceil_div(mnk[j][1], 128);
+    t128 += tiles[j] = ceil_div(mnk[j][0], 128) * ceil_div(mnk[j][1], 128);
+    steps[j] = std::max<int64_t>(1, ceil_div(mnk[j][2], kAnyBK));
+    if (tiles[j]) longest = std::max(longest, steps[j]);
   }
   s.tile = t256 >= kLinCus / 2 ? 256 : 128;
+  s.deep = s.tile == 128 && t128 <= kLinCus;
+  // Cut K so that no item is longer than the shortest length with which the
+  // items still run in one round.
+  int64_t len = longest;
+  if (s.deep) {
+    for (int64_t l = std::max<int64_t>(4, ceil_div(longest, kLinMaxSplits)); l < longest; ++l) {
+      int64_t items = 0;
+      for (int j = 0; j < jobs; ++j) items += tiles[j] * ceil_div(steps[j], l);
+      if (items <= kLinCus) {
+        len = l;
+        break;
+      }
+    }
+    if (longest - len < kLinSplitSteps) len = longest;
+  }
   size_t off = kCounterBytes;
   for (int j = 0; j < jobs; ++j) {
-    int64_t sp = 1;
-    const int64_t steps = ceil_div(mnk[j][2], kAnyBK);
-    if (s.tile == 128 && t128 && t128 < 2 * kLinCus)
-      sp = std::min<int64_t>({kLinMaxSplits, 2 * kLinCus / t128, steps / 4});
-    sp = std::max<int64_t>(sp, 1);
-    sp = ceil_div(std::max<int64_t>(steps, 1), ceil_div(std::max<int64_t>(steps, 1), sp));  // no empty range
+    int64_t sp = ceil_div(steps[j], len);
+    sp = ceil_div(steps[j], ceil_div(steps[j], sp));  // no empty range
     s.splits[j] = (int32_t)sp;
     s.partial_off[j] = off;
     if (sp > 1) off += aligned_up((size_t)(sp * mnk[j][0] * mnk[j][1]) * 4, 256);
@@ -549,6 +578,7 @@ extern "C" ovl_status gemm_epilogue_run(const gemm_epilogue_desc* desc, const vo
   args.job[0] = lin_job(s, 0, {static_cast<const uint16_t*>(a), d.lda, d.m, d.k},
                         {static_cast<const uint16_t*>(b), d.ldb, d.n, d.k}, e, workspace);
   args.sum.splits = 1;
+  if (s.deep) return lin_fwd_launch<Fwd128D>(args, stream);
   return s.tile == 256 ? lin_fwd_launch<Fwd256>(args, stream) : lin_fwd_launch<Fwd128>(args, stream);
 }
 
@@ -625,5 +655,6 @@ extern "C" ovl_status gemm_epilogue_grad_run(const gemm_epilogue_grad_desc* desc
     u.strips = (int32_t)ceil_div(d.n, 64);
     u.items = u.strips * u.splits;
   }
+  if (s.deep) return lin_grad_launch<Db128D, Da128D>(args, stream);
   return s.tile == 256 ? lin_grad_launch<Db256, Da256>(args, stream) : lin_grad_launch<Db128, Da128>(args, stream);
 }

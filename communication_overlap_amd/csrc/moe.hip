@@ -25,7 +25,7 @@ namespace ovl {
 namespace {
 
 constexpr int kMoeTokens = 128, kMoeExperts = 256, kMoeTopk = 8;
-constexpr int kMoeRouteRows = 128;   // rows of the router a workgroup sums
+constexpr int kMoeRouteRows = 64;    // rows of the router a workgroup sums (128: 8.8 against 3.4 us for a token)
 constexpr int kMoeRouteTokens = 4;   // tokens of a routing group (1 where there is one)
 // Arrival counters: down tiles, then (expert, up tile).
 constexpr int32_t kMoeDownCounters = 2048;

@@ -452,10 +452,12 @@ class _Buffers:
     as large as the call takes it to be (dense, or a two-dimensional view with
     the descriptor's row stride); raw addresses pass unchecked."""
 
+    __slots__ = ("where", "device")
+
     def __init__(self, where: str):
-        import torch
+        torch = _torch()
         self.where = where
-        self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+        self.device = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
 
     def refuse(self, name: str, why: str):
         raise OvlError(OVL_EINVAL, f"{self.where}: {name} {why}")
@@ -463,18 +465,39 @@ class _Buffers:
     def __call__(self, name: str, t, size: int, rows: int, cols: int, ld: int = 0):
         if t is None or isinstance(t, int):
             return t
-        if not t.is_cuda or t.get_device() != self.device:
+        if t.get_device() != self.device:  # -1: host memory
             self.refuse(name, "is not on the current device")
         if t.element_size() != size:
             self.refuse(name, f"has elements of {t.element_size()} bytes, not {size}")
-        ld = ld or cols
         if t.is_contiguous():
-            if rows > 0 and t.numel() < (rows - 1) * ld + cols:
+            if rows > 0 and t.numel() < (rows - 1) * (ld or cols) + cols:
                 self.refuse(name, "is too small")
-        elif not (t.dim() == 2 and t.stride(1) == 1 and t.stride(0) == ld and t.shape[0] >= rows
+        elif not (t.dim() == 2 and t.stride(1) == 1 and t.stride(0) == (ld or cols) and t.shape[0] >= rows
                   and t.shape[1] >= cols):
             self.refuse(name, "is neither dense nor a matrix with the descriptor's row stride")
         return t.data_ptr()
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
+
+
+def _workspace(buf, workspace, nbytes, desc):
+    """The workspace's address; its size is asked of the library once for a descriptor's contents."""
+    if workspace is None or isinstance(workspace, int):
+        return workspace
+    key = bytes(desc)
+    known = getattr(desc, "_workspace", None)
+    if known is None or known[0] != key:
+        known = desc._workspace = (key, nbytes(byref(desc)))
+    return buf("workspace", workspace, 1, 1, known[1])
 
 
 _SIZE = {BF16: 2, F32: 4, FP8: 1}
@@ -500,12 +523,6 @@ def gemm_epilogue_run(desc: GemmEpilogueDesc, a, b, bias, residual, out, z, work
         buf("out", out, _SIZE.get(desc.out_type, 1), m, n, desc.ldo), buf("z", z, 2, m, n, desc.ldz),
         _workspace(buf, workspace, lib().gemm_epilogue_workspace_bytes, desc), _stream(stream))
     return _check(st, "gemm_epilogue_run", raise_on_error)
-
-
-def _workspace(buf, workspace, nbytes, desc):
-    if workspace is None or isinstance(workspace, int):
-        return workspace
-    return buf("workspace", workspace, 1, 1, nbytes(byref(desc)))
 
 
 def gemm_epilogue_grad_desc(m, n, k, act="none", act_in="none", dy_type="bf16", da_type="bf16", db_type="f32", lda=0,
