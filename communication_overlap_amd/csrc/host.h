@@ -14,10 +14,12 @@ namespace ovl {
   } while (0)
 
 // The head of the feed-forward calls' workspaces: the error record, then
-// int32 arrival counters, zero between calls.  Nothing else lies there, so
-// that calls of different kinds and sizes may use one workspace in turn.
-constexpr size_t kCounterBytes = 65536;
-constexpr int32_t kCounters = (int32_t)(kCounterBytes - OVL_ERROR_RECORD_BYTES) / 4;
+// int32 arrival counters, zero between calls, one in 64 bytes (arrivals at
+// counters of one line queue up behind each other).  Nothing else lies there,
+// so that calls of different kinds and sizes may use one workspace in turn.
+constexpr size_t kCounterBytes = 262144;
+constexpr int kCounterStride = 16;
+constexpr int32_t kCounters = (int32_t)(kCounterBytes - OVL_ERROR_RECORD_BYTES) / (4 * kCounterStride);
 
 constexpr uint64_t kDefaultSpinLimit = 1ull << 22;
 

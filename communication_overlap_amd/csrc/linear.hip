@@ -260,19 +260,23 @@ __global__ __launch_bounds__(kThreads) void lin_row_kernel(LinRowArgs a) {
         row_sums8<C>(v, st, 0, row, (i % PR) * 8);
         store8_agent(v, p + row * a.n + col);
       }
-      if (!row_arrive_last(a.counters + tile, a.splits, &flag)) return;
+      if (!row_arrive_last(a.counters + tile * kCounterStride, a.splits, &flag)) return;
     }
     for (int i = threadIdx.x; i < pieces; i += kThreads) {
       const int row = i / PR;
       const int64_t col = o.col0 + (i % PR) * 8;
       if (col >= a.n) continue;
-      float v[8];
+      float v[1][8], bias[8];
+      // The epilogue's own loads go out with the sums'.
+      epilogue_bias(bias, a.epi, col, true);
+      const EpilogueIn x = epilogue_load(a.epi, row, col);
       if (a.splits > 1)
-        row_ranges8(v, a.partial + row * a.n + col, a.splits, a.m * a.n);
+        row_ranges8(v, a.partial + row * a.n + col, a.splits, a.m * a.n, 0);
       else
-        row_sums8<C>(v, st, 0, row, (i % PR) * 8);
-      epilogue8(a.epi, row, col, v);
+        row_sums8<C>(v[0], st, 0, row, (i % PR) * 8);
+      epilogue8(a.epi, row, col, v[0], bias, x);
     }
+    wave_drain();
   });
 }
 

@@ -28,7 +28,7 @@ constexpr int kMoeTokens = 128, kMoeExperts = 256, kMoeTopk = 8;
 constexpr int kMoeRouteRows = 64;    // rows of the router a workgroup sums (128: 8.8 against 3.4 us for a token)
 constexpr int kMoeRouteTokens = 4;   // tokens of a routing group (1 where there is one)
 // Arrival counters: down tiles, then (expert, up tile).
-constexpr int32_t kMoeDownCounters = 2048;
+constexpr int32_t kMoeDownCounters = 1024;
 constexpr int kMoeGroups = 256;  // workgroups of the experts' launches: one a compute unit
 
 struct MoeArgs {
@@ -217,6 +217,13 @@ struct MoeLds {
   int32_t flag;
 };
 
+// Codes: the column scales of even and odd units, gate's (or all) and up's.
+// Wavefront 0 fetches a unit's ahead of its steps, straight into LDS: loads of
+// them behind the products would wait for the next unit's weights.
+struct MoeScales {
+  float s[2][256];
+};
+
 // (Shared memory reached through the generator is named as such: a generic
 // load counts as a global one, and a wait for it would empty the rings.)
 __device__ inline int32_t lds_word(const int32_t* p) { return *OVL_LDS(const int32_t, p); }
@@ -287,13 +294,15 @@ struct MoeGen {
   static constexpr int N = C::ROWS;
   const MoeArgs& a;
   MoeLds<N>& s;
+  MoeScales* scales;  // codes only
   RowOperands o;
   int32_t tiles, ranges, steps, per, items;
   // The unit being loaded, and the unit being added up.
   int32_t l_item, l_first, l_count, l_unit;
   int32_t c_item, c_first, c_count, c_unit;
 
-  __device__ inline MoeGen(const MoeArgs& args, MoeLds<N>& lds, int active) : a(args), s(lds), o{} {
+  __device__ inline MoeGen(const MoeArgs& args, MoeLds<N>& lds, MoeScales* sc, int active)
+      : a(args), s(lds), scales(sc), o{} {
     tiles = UP ? a.up_tiles : a.down_tiles;
     steps = UP ? a.up_steps : a.down_steps;
     ranges = moe_ranges(active * tiles, steps, UP ? a.up_max : a.down_max);
@@ -339,6 +348,16 @@ struct MoeGen {
     o.w = (UP ? a.w1 : a.w2) + e * o.w_bytes;
     o.col0 = (int64_t)tile(l_item) * C::COLS;
     ld.init(o, table, UP ? a.topk_n : 1);
+    if constexpr (C::FP8) {
+      static_assert((C::PAIR ? 2 : 1) * C::COLS <= 256, "a unit's scales fit one load");
+      if (uniform((int)(threadIdx.x >> 6)) == 0) {
+        const int64_t n = UP ? a.n1 : a.hidden;
+        const u32x4 srd = make_srd((UP ? a.s1 : a.s2) + e * n, n * 4);
+        const int half = lane_id() / (C::COLS / 4), c = lane_id() % (C::COLS / 4) * 4;
+        const bool there = half < (C::PAIR ? 2 : 1) && o.col0 + c < o.cols;
+        load_to_lds(srd, lds_addr(scales->s[u & 1]), there ? (uint32_t)(half * o.pair + o.col0 + c) * 4 : kOOB);
+      }
+    }
     steps_of(l_item, s0, s1);
     return true;
   }
@@ -388,13 +407,17 @@ __device__ inline void moe_act(const MoeArgs& a, int planes, int pair, int64_t c
   moe_store_h(a, planes, pair, col, g);
 }
 
+// v times the scales of columns col .. of half `half` of unit u.
 template <class C>
-__device__ inline void moe_scale(float (&v)[8], const float* s, int64_t i) {
-  if (C::FP8) {
-    float w[8];
-    load8(w, s, i, OVL_F32);
+__device__ inline void moe_scale(float (&v)[8], const MoeScales* sc, int32_t u, int half, int col) {
+  if constexpr (C::FP8) {
+    const float* p = sc->s[u & 1] + half * C::COLS + col;
+    const f32x4 a = *OVL_LDS(const f32x4, p), b = *OVL_LDS(const f32x4, p + 4);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] *= w[c];
+    for (int c = 0; c < 4; ++c) {
+      v[c] *= a[c];
+      v[4 + c] *= b[c];
+    }
   }
 }
 
@@ -402,9 +425,11 @@ template <class C>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a, int planes) {
   extern __shared__ __align__(16) uint8_t moe_lds[];
   __shared__ MoeLds<C::ROWS> s;
+  __shared__ __align__(16) uint8_t sc[C::FP8 ? sizeof(MoeScales) : 16];
+  MoeScales* scales = reinterpret_cast<MoeScales*>(sc);
   constexpr int PR = C::COLS / 8;  // pieces of a row
   const int active = moe_begin(a, s);
-  MoeGen<C, true> gen(a, s, active);
+  MoeGen<C, true> gen(a, s, scales, active);
   row_stream<C>(gen, moe_lds, [&](int32_t u, const float* st) {
     const int item = gen.c_item, sp = gen.range_of(item), tile = gen.tile(item);
     const int e = uniform(lds_word(s.experts + gen.slot(item)));
@@ -416,10 +441,10 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a, int planes)
       if (pair < 0 || col >= a.inter) continue;
       float g[8], v[8];
       row_sums8<C>(g, st, 0, i / PR, (i % PR) * 8);
-      moe_scale<C>(g, a.s1, e * a.n1 + col);
+      moe_scale<C>(g, scales, u, 0, (i % PR) * 8);
       if (C::PAIR) {
         row_sums8<C>(v, st, 1, i / PR, (i % PR) * 8);
-        moe_scale<C>(v, a.s1, e * a.n1 + a.inter + col);
+        moe_scale<C>(v, scales, u, 1, (i % PR) * 8);
       }
       if (gen.ranges > 1) {
         float* p = a.up + ((int64_t)sp * a.pairs + pair) * a.n1 + col;
@@ -430,32 +455,53 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a, int planes)
       }
     }
     if (gen.ranges == 1 || !gen.last_of_item()) return;
-    if (!row_arrive_last(a.up_counters + gen.slot(item) * gen.tiles + tile, gen.ranges, &s.flag)) return;
+    if (!row_arrive_last(a.up_counters + (gen.slot(item) * gen.tiles + tile) * kCounterStride, gen.ranges, &s.flag)) return;
     // All the expert's pairs, in the order of their ids.
     for (int i = threadIdx.x; i < a.pairs * PR; i += kThreads) {
       const int pair = i / PR;
       const int64_t col = col0 + (i % PR) * 8;
       if (lds_word(s.ids + pair) != e || col >= a.inter) continue;
-      float g[8], v[8];
-      const float* p = a.up + pair * a.n1 + col;
-      row_ranges8(g, p, gen.ranges, a.pairs * a.n1);
-      if (C::PAIR) row_ranges8(v, p + a.inter, gen.ranges, a.pairs * a.n1);
-      moe_act<C>(a, planes, pair, col, g, v);
+      float v[C::PAIR ? 2 : 1][8];
+      row_ranges8(v, a.up + pair * a.n1 + col, gen.ranges, a.pairs * a.n1, a.inter);
+      moe_act<C>(a, planes, pair, col, v[0], v[C::PAIR ? 1 : 0]);
     }
+    wave_drain();
   });
 }
 
-// Eight columns of a token's output: its choices in order.
+// Eight columns of a token's output: its choices in order, each the sum of its
+// ranges in order; eight loads of (choice, range) go out together.
 __device__ inline void moe_out8(const MoeArgs& a, const int32_t* ids, int ranges, int t, int64_t col) {
-  float v[8] = {};
-  for (int j = 0; j < a.topk_n; ++j) {
-    const int pair = t * a.topk_n + j;
-    if (lds_word(ids + pair) < 0) continue;
-    float y[8];
-    row_ranges8(y, a.down + pair * a.hidden + col, ranges, a.pairs * a.hidden);
-    const float g = a.gates[pair];
+  constexpr int U = 8;
+  float v[8] = {}, y[8] = {};
+  int lj = 0, ls = 0, cj = 0, cs = 0;  // the (choice, range) loaded next and added next
+  while (cj < a.topk_n) {
+    RowPart q[U];
+    float gate[U];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] += g * y[c];
+    for (int u = 0; u < U; ++u) {
+      const int pair = t * a.topk_n + lj;
+      if (lj < a.topk_n && lds_word(ids + pair) >= 0) {
+        q[u] = load8_agent(a.down + ((int64_t)ls * a.pairs + pair) * a.hidden + col);
+        gate[u] = a.gates[pair];
+      }
+      if (++ls == ranges) ls = 0, ++lj;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int pair = t * a.topk_n + cj;
+      if (cj < a.topk_n && lds_word(ids + pair) >= 0) {
+        add8(y, q[u]);
+        if (cs + 1 == ranges) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            v[c] += gate[u] * y[c];
+            y[c] = 0.f;
+          }
+        }
+      }
+      if (++cs == ranges) cs = 0, ++cj;
+    }
   }
   store8(v, a.out, t * a.hidden + col, a.out_type);
 }
@@ -467,18 +513,20 @@ __device__ inline void moe_out(const MoeArgs& a, const int32_t* ids, int ranges,
     if (col0 + (i % PR) * 8 < a.hidden) moe_out8(a, ids, ranges, i / PR, col0 + (i % PR) * 8);
 }
 
-template <class C>
+// FUSED: the launch sums the choices itself.
+template <class C, bool FUSED>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
   extern __shared__ __align__(16) uint8_t moe_lds[];
   __shared__ MoeLds<C::ROWS> s;
+  __shared__ __align__(16) uint8_t sc[C::FP8 ? sizeof(MoeScales) : 16];
+  MoeScales* scales = reinterpret_cast<MoeScales*>(sc);
   constexpr int PR = C::COLS / 8;
   const int active = moe_begin(a, s);
-  if (active == 0 && a.fused)  // no expert of this rank: zeros
+  if (FUSED && active == 0)  // no expert of this rank: zeros
     for (int t = blockIdx.x; t < a.down_tiles; t += gridDim.x) moe_out<PR>(a, s.ids, 1, (int64_t)t * C::COLS);
-  MoeGen<C, false> gen(a, s, active);
+  MoeGen<C, false> gen(a, s, scales, active);
   row_stream<C>(gen, moe_lds, [&](int32_t u, const float* st) {
     const int item = gen.c_item, sp = gen.range_of(item), tile = gen.tile(item);
-    const int e = uniform(lds_word(s.experts + gen.slot(item)));
     const int64_t col0 = (int64_t)tile * C::COLS;
     const int32_t* rows = gen.rows(u);
     for (int i = threadIdx.x; i < C::PIECES; i += kThreads) {
@@ -487,15 +535,17 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
       if (pair < 0 || col >= a.hidden) continue;
       float v[8];
       row_sums8<C>(v, st, 0, i / PR, (i % PR) * 8);
-      moe_scale<C>(v, a.s2, e * a.hidden + col);
+      moe_scale<C>(v, scales, u, 0, (i % PR) * 8);
       float* p = a.down + ((int64_t)sp * a.pairs + pair) * a.hidden + col;
-      if (a.fused)
+      if (FUSED)
         store8_agent(v, p);
       else
         store8(v, p, 0, OVL_F32);
     }
-    if (a.fused && gen.last_of_item() && row_arrive_last(a.down_counters + tile, active * gen.ranges, &s.flag))
+    if (FUSED && gen.last_of_item() && row_arrive_last(a.down_counters + tile * kCounterStride, active * gen.ranges, &s.flag)) {
       moe_out<PR>(a, s.ids, gen.ranges, col0);
+      wave_drain();
+    }
   });
 }
 
@@ -515,7 +565,7 @@ __global__ __launch_bounds__(kThreads) void moe_sum_kernel(MoeArgs a) {
 
 struct MoeShape {
   int32_t pairs, planes, chunks;
-  bool few;  // few tokens an expert
+  bool few, many;  // pairs an expert: at most 1.5, more than 6
   int32_t up_tiles, up_max, up_steps;
   int32_t down_tiles, down_max, down_steps;
   size_t h_off, up_off, down_off, logits_off, bytes;
@@ -539,6 +589,7 @@ MoeShape moe_shape(const moe_layer_desc& d) {
   s.planes = d.out_type == OVL_F32 ? 3 : 2;
   s.chunks = (int32_t)ceil_div(d.hidden, kMoeRouteRows);
   s.few = 2 * s.pairs <= 3 * d.experts;
+  s.many = s.pairs > 6 * d.experts;
   s.up_tiles = (int32_t)ceil_div(d.inter, fp8 && d.gated ? 32 : 64);
   s.down_tiles = (int32_t)ceil_div(d.hidden, fp8 ? 64 : 128);
   s.up_steps = (int32_t)ceil_div(d.hidden, ks);
@@ -588,9 +639,10 @@ ovl_status moe_up(const MoeArgs& a, int planes, hipStream_t stream) {
 
 template <class C>
 ovl_status moe_down(const MoeArgs& a, hipStream_t stream) {
-  ovl_status st = allow_lds(reinterpret_cast<const void*>(&moe_down_kernel<C>), C::LDS);
+  const auto kernel = a.fused ? &moe_down_kernel<C, true> : &moe_down_kernel<C, false>;
+  ovl_status st = allow_lds(reinterpret_cast<const void*>(kernel), C::LDS);
   if (st) return st;
-  hipLaunchKernelGGL((moe_down_kernel<C>), dim3(kMoeGroups), dim3(kThreads), C::LDS, stream, a);
+  hipLaunchKernelGGL(kernel, dim3(kMoeGroups), dim3(kThreads), C::LDS, stream, a);
   OVL_HIP_TRY(hipGetLastError());
   if (!a.fused) {
     hipLaunchKernelGGL((moe_sum_kernel<C>), dim3(ceil_div(a.tokens * a.hidden / 8, kThreads)), dim3(kThreads), 0, stream,
@@ -613,7 +665,9 @@ ovl_status moe_route(const MoeArgs& a, hipStream_t stream) {
   return OVL_OK;
 }
 
-// bf16 weights: NB blocks of 16 rows a unit.
+// bf16 weights: NB blocks of 16 rows a unit.  Two where experts have many
+// tokens; their rows take a slot from the down launch's ring (64 tokens, top 2
+// of 64: 133 us with two blocks, 113 with one).
 template <int NB>
 ovl_status moe_bf16(const MoeArgs& a, bool gated, int planes, hipStream_t stream) {
   const ovl_status st = gated ? moe_up<RowCfg<false, true, 1, NB, 1, kMoeRing>>(a, planes, stream)
@@ -683,7 +737,7 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
   a.down = reinterpret_cast<float*>(ws + s.down_off);
   a.logits = reinterpret_cast<double*>(ws + s.logits_off);
   a.down_counters = reinterpret_cast<int32_t*>(ws + OVL_ERROR_RECORD_BYTES);
-  a.up_counters = a.down_counters + kMoeDownCounters;
+  a.up_counters = a.down_counters + kMoeDownCounters * kCounterStride;
   a.hidden = d->hidden;
   a.inter = d->inter;
   a.n1 = d->gated ? 2 * d->inter : d->inter;
@@ -708,5 +762,5 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
     if (st) return st;
   }
   if (fp8) return moe_fp8(a, d->gated, s.planes, s.few, stream);
-  return d->tokens <= 16 ? moe_bf16<1>(a, d->gated, s.planes, stream) : moe_bf16<2>(a, d->gated, s.planes, stream);
+  return s.many ? moe_bf16<2>(a, d->gated, s.planes, stream) : moe_bf16<1>(a, d->gated, s.planes, stream);
 }

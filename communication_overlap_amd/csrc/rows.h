@@ -250,7 +250,9 @@ __device__ inline void row_wait(int steps) {
 //     inside the product loop, where a wait would empty the ring.
 //     It is called at most one unit ahead of done().
 //   gen.range(u, s0, s1): the range alone.
-//   done(u, sums): unit u's sums of all four wavefronts, staged in LDS as
+//   done(u, sums): (a path of it that loads from global memory ends with
+//     wave_drain(): a load of which the compiler cannot tell that it has landed
+//     would make it wait in the product loop) unit u's sums of all four wavefronts, staged in LDS as
 //     sums[tile][row][TC + 4], in every thread's sight.
 // Every sum is made of the waves' in an order fixed by its columns, each
 // wave's in k order.
@@ -325,7 +327,6 @@ __device__ inline void row_stream(Gen& gen, uint8_t* lds, Done done) {
       __syncthreads();
     }
     done(u, st);
-    wave_drain();  // done's loads are known to have landed: no wait for them inside the product loop
   }
 }
 
@@ -351,33 +352,54 @@ __device__ inline void store8_agent(const float (&v)[8], float* p) {
               (uint64_t)__builtin_bit_cast(uint32_t, v[2 * c]) | (uint64_t)__builtin_bit_cast(uint32_t, v[2 * c + 1]) << 32);
 }
 
+// Partial products written by other workgroups of the launch (store8_agent):
+// agent-scope loads need no acquire, which would empty the die's caches.
+struct RowPart {
+  uint64_t q[4];
+};
+__device__ inline RowPart load8_agent(const float* p) {
+  RowPart r;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    r.q[c] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p) + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return r;
+}
+__device__ inline void add8(float (&v)[8], const RowPart& r) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    v[2 * c] += __builtin_bit_cast(float, (uint32_t)r.q[c]);
+    v[2 * c + 1] += __builtin_bit_cast(float, (uint32_t)(r.q[c] >> 32));
+  }
+}
+
 // Eight sums of `ranges` partial products, `stride` floats apart, added in
-// range order; four ranges' loads go out together.
-__device__ inline void row_ranges8(float (&v)[8], const float* p, int ranges, int64_t stride) {
+// range order; H such sets, `half` floats apart.  Eight ranges' loads of all
+// sets go out together: the reader's time is the latency of its batches.
+template <int H>
+__device__ inline void row_ranges8(float (&v)[H][8], const float* p, int ranges, int64_t stride, int64_t half) {
+  constexpr int U = 8;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) v[c] = 0.f;
-  for (int s = 0; s < ranges; s += 4) {
-    f32x4 q[4][2];
+  for (int h = 0; h < H; ++h)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const f32x4* r = reinterpret_cast<const f32x4*>(p + min(s + u, ranges - 1) * stride);
-      q[u][0] = r[0];
-      q[u][1] = r[1];
-    }
+    for (int c = 0; c < 8; ++c) v[h][c] = 0.f;
+  for (int s = 0; s < ranges; s += U) {
+    RowPart q[U][H];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (s + u < ranges)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          v[c] += q[u][0][c];
-          v[4 + c] += q[u][1][c];
-        }
+      for (int h = 0; h < H; ++h)
+        if (s + u < ranges) q[u][h] = load8_agent(p + (s + u) * stride + h * half);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (s + u < ranges) add8(v[h], q[u][h]);
   }
 }
 
 // Arrival at a counter of `expected` workgroups: true, in every thread, for
-// the last one, which has acquired the others' stores and returned the
-// counter to zero.
+// the last one, which has returned the counter to zero and finds the others'
+// agent-scope stores with agent-scope loads.
 __device__ inline bool row_arrive_last(int32_t* counter, int expected, int32_t* lds_flag) {
   wave_drain();
   __syncthreads();
@@ -387,9 +409,7 @@ __device__ inline bool row_arrive_last(int32_t* counter, int expected, int32_t* 
     if (old + 1 == expected) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  const bool last = uniform(*lds_flag);
-  if (last) wave_acquire();
-  return last;
+  return uniform(*lds_flag);
 }
 
 }  // namespace ovl
