@@ -324,9 +324,12 @@ struct LinShape {
 
 constexpr int kLinCus = 256;  // the plan is made for a whole MI355X, so that sizes do not hang on the device
 
-// What a second launch costs, in K steps of a 128 x 128 tile (about 6 us of
-// 0.4): below that many saved, a tile is not cut.
-constexpr int64_t kLinSplitSteps = 16;
+// What cutting K costs and saves, in microseconds: a step of a 128 x 128 tile
+// alone on its compute unit, a second launch, and a float32 partial product's
+// way to memory and back (8 bytes an element at 4 TB/s).  33 x 256 x 1024 ran
+// in 8.7 us cut and 12.8 whole; 512 x 1024 x 2048 in 20.4 us cut in eight, and
+// less in four.
+constexpr double kLinStepUs = 0.4, kLinLaunchUs = 1.0, kLinPartialUs = 8.0 / 4e6;
 
 LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum_n) {
   LinShape s = {};
@@ -339,19 +342,36 @@ LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum
   }
   s.tile = t256 >= kLinCus / 2 ? 256 : 128;
   s.deep = s.tile == 128 && t128 <= kLinCus;
-  // Cut K so that no item is longer than the shortest length with which the
-  // items still run in one round.
+  // Cut K where few tiles have many steps.  Items that all run at once: into
+  // the length that costs least.  More of them: a product whose tiles are over
+  // half again as long as a compute unit's share of all the work is cut to that
+  // share (64 x 7168 x 8192, gradient: 32 tiles of 112 steps beside 896 of one;
+  // 128 us whole, 81 cut).
   int64_t len = longest;
   if (s.deep) {
-    for (int64_t l = std::max<int64_t>(4, ceil_div(longest, kLinMaxSplits)); l < longest; ++l) {
+    double best = kLinStepUs * longest;
+    for (int64_t c = 2; c <= kLinMaxSplits; ++c) {
+      const int64_t l = ceil_div(longest, c);
       int64_t items = 0;
-      for (int j = 0; j < jobs; ++j) items += tiles[j] * ceil_div(steps[j], l);
-      if (items <= kLinCus) {
+      double cost = kLinStepUs * l + kLinLaunchUs;
+      for (int j = 0; j < jobs; ++j) {
+        const int64_t cuts = ceil_div(steps[j], l);
+        items += tiles[j] * cuts;
+        if (cuts > 1) cost += kLinPartialUs * cuts * mnk[j][0] * mnk[j][1];
+      }
+      if (items > kLinCus) break;
+      if (cost < best) {
+        best = cost;
         len = l;
-        break;
       }
     }
-    if (longest - len < kLinSplitSteps) len = longest;
+  } else {
+    int64_t work = 0;
+    for (int j = 0; j < jobs; ++j)
+      work += ceil_div(mnk[j][0], s.tile) * ceil_div(mnk[j][1], s.tile) * steps[j];
+    const int64_t share = std::max<int64_t>({8, ceil_div(work, s.tile == 256 ? kLinCus : 2 * kLinCus),
+                                             ceil_div(longest, kLinMaxSplits)});
+    if (2 * longest > 3 * share) len = share;
   }
   size_t off = kCounterBytes;
   for (int j = 0; j < jobs; ++j) {

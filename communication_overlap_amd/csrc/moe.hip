@@ -217,11 +217,13 @@ struct MoeLds {
   int32_t flag;
 };
 
-// Codes: the column scales of even and odd units, gate's (or all) and up's.
+// Codes: the column scales of the last four units, gate's (or all) and up's.
 // Wavefront 0 fetches a unit's ahead of its steps, straight into LDS: loads of
-// them behind the products would wait for the next unit's weights.
+// them behind the products would wait for the next unit's weights.  It may be
+// one unit ahead of the unit whose steps run, and a slower wavefront one
+// behind: three are in use at a time.
 struct MoeScales {
-  float s[2][256];
+  float s[4][256];
 };
 
 // (Shared memory reached through the generator is named as such: a generic
@@ -355,7 +357,7 @@ struct MoeGen {
         const u32x4 srd = make_srd((UP ? a.s1 : a.s2) + e * n, n * 4);
         const int half = lane_id() / (C::COLS / 4), c = lane_id() % (C::COLS / 4) * 4;
         const bool there = half < (C::PAIR ? 2 : 1) && o.col0 + c < o.cols;
-        load_to_lds(srd, lds_addr(scales->s[u & 1]), there ? (uint32_t)(half * o.pair + o.col0 + c) * 4 : kOOB);
+        load_to_lds(srd, lds_addr(scales->s[u & 3]), there ? (uint32_t)(half * o.pair + o.col0 + c) * 4 : kOOB);
       }
     }
     steps_of(l_item, s0, s1);
@@ -411,7 +413,7 @@ __device__ inline void moe_act(const MoeArgs& a, int planes, int pair, int64_t c
 template <class C>
 __device__ inline void moe_scale(float (&v)[8], const MoeScales* sc, int32_t u, int half, int col) {
   if constexpr (C::FP8) {
-    const float* p = sc->s[u & 1] + half * C::COLS + col;
+    const float* p = sc->s[u & 3] + half * C::COLS + col;
     const f32x4 a = *OVL_LDS(const f32x4, p), b = *OVL_LDS(const f32x4, p + 4);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {

@@ -184,6 +184,44 @@ def test_not_finite_weights_of_other_experts_do_not_leak():
     c.check()
 
 
+def test_every_e4m3_code_is_widened_exactly():
+    """x picks one code a token, the second weight copies it out: the output is
+    the code's value, over all 254 finite codes (subnormals and both zeros)."""
+    t = fu.torch()
+    c = Moe(128, 256, 16, 1, 1, "fp8", "f32", "none", False, route=False, seed=1)
+    codes = np.arange(256, dtype=np.uint8)
+    codes[[0x7F, 0xFF]] = 0  # the NaN codes: zero times NaN would reach every token
+    c.w1.zero_()
+    c.w1[0, 3] = t.from_numpy(codes).cuda()
+    c.w2.zero_()
+    c.w2[0, 5, 3] = 0x38  # 1.0
+    c.s1.fill_(1.0)
+    c.s2.fill_(1.0)
+    c.ids.zero_()
+    c.gates.fill_(1.0)
+    for half in range(2):
+        c.x.zero_()
+        c.x[t.arange(128), t.arange(128) + 128 * half] = 1.0
+        c.run()
+        want = oracle.e4m3_decode(codes[128 * half:128 * (half + 1)])
+        assert np.array_equal(fu.f64(c.out[:128, 5]), want)
+        rest = c.out[:128].clone()
+        rest[:, 5] = 0
+        assert not bool(rest.any())
+
+
+@pytest.mark.parametrize("w,out", [("bf16", "f32"), ("fp8", "f32"), ("fp8", "bf16")])
+@pytest.mark.parametrize("E,T,K", [(2, 128, 2), (16, 100, 8)])
+def test_many_units_a_workgroup(w, out, E, T, K):
+    """Many short units in turn: few steps each, rows over several groups."""
+    c = Moe(T, 2048, 48, E, K, w, out, seed=21)
+    c.run()
+    c.check()
+    d = Moe(T, 48, 4096, E, K, w, out, seed=22)
+    d.run()
+    d.check()
+
+
 def test_weights_past_four_gib():
     """Experts whose weights lie past 32-bit offsets."""
     t, o = fu.torch(), ovl()
