@@ -381,7 +381,10 @@ LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum
     s.partial_off[j] = off;
     if (sp > 1) off += aligned_up((size_t)(sp * mnk[j][0] * mnk[j][1]) * 4, 256);
   }
-  s.sum_splits = (int32_t)std::min<int64_t>(64, std::max<int64_t>(1, sum_m / 8192));
+  // Column sums: a workgroup adds a strip's rows at the latency of its loads, so
+  // few strips are cut into ranges of rows (7936 x 16: 16 us in one).
+  const int64_t strips = std::max<int64_t>(1, ceil_div(sum_n, 64));
+  s.sum_splits = (int32_t)std::max<int64_t>({1, std::min<int64_t>(sum_m / 1024, 64 / strips), std::min<int64_t>(sum_m / 16384, 64)});
   s.sum_off = off;
   if (s.sum_splits > 1) off += aligned_up((size_t)s.sum_splits * sum_n * 4, 256);
   s.bytes = off;

@@ -757,7 +757,9 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
   a.down_max = s.down_max;
   a.down_steps = s.down_steps;
   a.chunks = s.chunks;
-  a.fused = (int64_t)s.pairs * s.down_tiles <= kMoeGroups;  // at most one unit a workgroup
+  // At most one unit a workgroup, and no more tokens than one workgroup sums at
+  // once (40 tokens of 112 columns: 22 us so, 12 with a launch for the sum).
+  a.fused = (int64_t)s.pairs * s.down_tiles <= kMoeGroups && s.pairs <= 8 * d->topk;
   if (router) {
     st = d->experts <= 64 ? moe_route<64>(a, stream)
                           : (d->experts <= 128 ? moe_route<128>(a, stream) : moe_route<256>(a, stream));
