@@ -233,6 +233,7 @@ struct LinRowGen {
     if (u == 0) ld.init(*o, rows);
     return range(u, a, b);
   }
+  __device__ inline int32_t turn(int32_t) const { return 0; }
 };
 
 template <class C>

@@ -384,6 +384,8 @@ struct MoeGen {
     steps_of(c_item, s0, s1);
     return true;
   }
+  // Codes: units start at different places of their range.
+  __device__ inline int32_t turn(int32_t n) const { return C::FP8 ? tile(l_item) * 5 % n : 0; }
   __device__ inline bool last_of_item() const { return c_first + N >= c_count; }
 };
 

@@ -269,9 +269,12 @@ __device__ inline void row_stream(Gen& gen, uint8_t* lds, Done done) {
   const uint32_t ring_a = lds_addr(ring);
   float* st = reinterpret_cast<float*>(lds + kRowWaves * C::WAVE_LDS);
   // The unit being loaded, its next step and how many this wave has of it.
-  int32_t lu = 0, li = 0, ln = 0, l0 = 0, l1 = 0;
+  int32_t lu = 0, li = 0, ln = 0, l0 = 0, l1 = 0, turn = 0;
   bool more = gen.begin(0, ld, l0, l1);
-  if (more) ln = steps_of(l0, l1);
+  if (more) {
+    ln = steps_of(l0, l1);
+    turn = gen.turn(l1 - l0);
+  }
   int32_t islot = 0, uslot = 0, ahead = 0;  // ahead: steps issued and not yet used
   int32_t u = 0;                            // the unit being added up
   const auto issue_next = [&]() {
@@ -279,9 +282,12 @@ __device__ inline void row_stream(Gen& gen, uint8_t* lds, Done done) {
       more = gen.begin(++lu, ld, l0, l1);
       li = 0;
       ln = more ? steps_of(l0, l1) : 0;
+      turn = more ? gen.turn(l1 - l0) : 0;
     }
     if (!more || li == ln) return;
-    ld.issue(ring_a + islot * C::STEP, (l0 + wave + li * kRowWaves) * C::KS);
+    int32_t at = wave + li * kRowWaves + turn;  // the range's steps from `turn` on, and round
+    if (at >= l1 - l0) at -= l1 - l0;
+    ld.issue(ring_a + islot * C::STEP, (l0 + at) * C::KS);
     islot = islot + 1 == C::D ? 0 : islot + 1;
     ++li;
     ++ahead;

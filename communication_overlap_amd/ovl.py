@@ -213,6 +213,17 @@ def lib() -> ctypes.CDLL:
     return L
 
 
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
+
+
 def strerror(status: int) -> str:
     try:
         return lib().ovl_strerror(status).decode()
@@ -230,7 +241,12 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int:
     if stream is None:
-        import torch
+        # torch.cuda.current_stream() makes a Stream object (2.9 us a call); the
+        # handle alone takes 0.1.
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -478,17 +494,6 @@ class _Buffers:
         return t.data_ptr()
 
 
-def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
-
-
-_torch_module = None
-
-
 def _workspace(buf, workspace, nbytes, desc):
     """The workspace's address; its size is asked of the library once for a descriptor's contents."""
     if workspace is None or isinstance(workspace, int):
@@ -602,16 +607,13 @@ class GradClipPlan:
         h = c_void_p()
         _check(lib().grad_clip_plan(arr, len(src), byref(h)), "grad_clip_plan", True)
         self.handle = h
+        self.workspace_bytes = lib().grad_clip_workspace_bytes(h)
 
     def __del__(self):
         h = getattr(self, "handle", None)
         if h is not None and h.value and _lib is not None:
             _lib.grad_clip_plan_destroy(h)
             self.handle = None
-
-    @property
-    def workspace_bytes(self) -> int:
-        return lib().grad_clip_workspace_bytes(self.handle)
 
 
 def grad_clip_plan(src, dst=None) -> GradClipPlan:
