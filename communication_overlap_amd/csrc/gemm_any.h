@@ -42,6 +42,14 @@ struct AnyOperand {
 
 constexpr int kAnyBK = 64;
 
+// Chunk permutation of row k of a K-strided operand's LDS rows of R columns: a
+// fragment read takes 4 rows x 2 chunks per 16 lanes, rows 8 apart in
+// neighbouring groups of lanes.
+template <int R>
+__device__ inline uint32_t any_swz(uint32_t k) {
+  return R >= 128 ? swz_b(k) : 2 * ((k & 3) ^ ((k >> 3) & 1));
+}
+
 template <int R, int NW, bool KC>
 struct AnySide {
   static constexpr int BYTES = R * kAnyBK * 2;              // of one stage
@@ -60,7 +68,7 @@ struct AnySide {
   int32_t k;
   uint32_t lds;      // byte offset of this wave's first block within a stage
 
-  static __device__ inline uint32_t swz(uint32_t r) { return KC ? swz_a<64>(r) : swz_b(r); }
+  static __device__ inline uint32_t swz(uint32_t r) { return KC ? swz_a<64>(r) : any_swz<R>(r); }
 
   __device__ inline void init(const AnyOperand& o, int64_t r0, uint32_t wave) {
     const uint32_t l = lane_id();
@@ -113,7 +121,7 @@ struct AnyFrag {
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const uint32_t col = w0 + f * 32 + (g & 1) * 16 + 4 * (s & 3);
-        o[f] = brow * (R * 2) + ((col >> 3) ^ swz_b(brow)) * 16 + (col & 4) * 2;
+        o[f] = brow * (R * 2) + ((col >> 3) ^ any_swz<R>(brow)) * 16 + (col & 4) * 2;
       }
     }
   }

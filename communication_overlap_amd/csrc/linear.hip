@@ -308,16 +308,15 @@ using Da256 = AnyTile<256, 256, 8, true, true>;
 using Da128 = AnyTile<128, 128, 4, true, true>;
 using Db256 = AnyTile<256, 256, 8, false, false>;
 using Db128 = AnyTile<128, 128, 4, false, false>;
-// The same, four stages deep: one workgroup a compute unit.
-using Fwd128D = AnyTile<128, 128, 4, true, false, 4>;
-using Da128D = AnyTile<128, 128, 4, true, true, 4>;
-using Db128D = AnyTile<128, 128, 4, false, false, 4>;
+// Few tiles: half the rows, three stages deep, two workgroups a compute unit.
+using Fwd64 = AnyTile<64, 128, 4, true, false, 3>;
+using Da64 = AnyTile<64, 128, 4, true, true, 3>;
+using Db64 = AnyTile<64, 128, 4, false, false, 3>;
 
 // Tile edge and K splits of the products of one launch.  Both the size
 // queries and the launches use this.
 struct LinShape {
-  int tile;
-  bool deep;  // 128 x 128 tiles, at most one item a compute unit
+  int tile_m, tile_n;  // 256 x 256, 128 x 128 or 64 x 128
   int32_t splits[2];
   int32_t sum_splits;
   size_t partial_off[2], sum_off, bytes;
@@ -334,22 +333,29 @@ constexpr double kLinStepUs = 0.4, kLinLaunchUs = 1.0, kLinPartialUs = 8.0 / 4e6
 
 LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum_n) {
   LinShape s = {};
-  int64_t t256 = 0, t128 = 0, steps[2] = {1, 1}, tiles[2] = {}, longest = 1;
+  const auto tiles_of = [&](int j, int64_t tm, int64_t tn) {
+    return ceil_div(mnk[j][0], tm) * ceil_div(mnk[j][1], tn);
+  };
+  int64_t t256 = 0, t64 = 0, steps[2] = {1, 1}, tiles[2] = {}, longest = 1;
   for (int j = 0; j < jobs; ++j) {
-    t256 += ceil_div(mnk[j][0], 256) * ceil_div(mnk[j][1], 256);
-    t128 += tiles[j] = ceil_div(mnk[j][0], 128) * ceil_div(mnk[j][1], 128);
+    t256 += tiles_of(j, 256, 256);
+    t64 += tiles_of(j, 64, 128);
     steps[j] = std::max<int64_t>(1, ceil_div(mnk[j][2], kAnyBK));
-    if (tiles[j]) longest = std::max(longest, steps[j]);
+    if (mnk[j][0]) longest = std::max(longest, steps[j]);
   }
-  s.tile = t256 >= kLinCus / 2 ? 256 : 128;
-  s.deep = s.tile == 128 && t128 <= kLinCus;
+  // 256 x 256 where such tiles fill half the chip; 64 x 128 where even those
+  // run all at once; 128 x 128 between.
+  const bool few = t64 <= 2 * kLinCus;
+  s.tile_m = t256 >= kLinCus / 2 ? 256 : (few ? 64 : 128);
+  s.tile_n = s.tile_m == 256 ? 256 : 128;
+  for (int j = 0; j < jobs; ++j) tiles[j] = tiles_of(j, s.tile_m, s.tile_n);
   // Cut K where few tiles have many steps.  Items that all run at once: into
   // the length that costs least.  More of them: a product whose tiles are over
   // half again as long as a compute unit's share of all the work is cut to that
   // share (64 x 7168 x 8192, gradient: 32 tiles of 112 steps beside 896 of one;
   // 128 us whole, 81 cut).
   int64_t len = longest;
-  if (s.deep) {
+  if (s.tile_m == 64) {
     double best = kLinStepUs * longest;
     for (int64_t c = 2; c <= kLinMaxSplits; ++c) {
       const int64_t l = ceil_div(longest, c);
@@ -360,7 +366,7 @@ LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum
         items += tiles[j] * cuts;
         if (cuts > 1) cost += kLinPartialUs * cuts * mnk[j][0] * mnk[j][1];
       }
-      if (items > kLinCus) break;
+      if (items > 2 * kLinCus) break;
       if (cost < best) {
         best = cost;
         len = l;
@@ -368,9 +374,8 @@ LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum
     }
   } else {
     int64_t work = 0;
-    for (int j = 0; j < jobs; ++j)
-      work += ceil_div(mnk[j][0], s.tile) * ceil_div(mnk[j][1], s.tile) * steps[j];
-    const int64_t share = std::max<int64_t>({8, ceil_div(work, s.tile == 256 ? kLinCus : 2 * kLinCus),
+    for (int j = 0; j < jobs; ++j) work += tiles[j] * steps[j];
+    const int64_t share = std::max<int64_t>({8, ceil_div(work, s.tile_m == 256 ? kLinCus : 2 * kLinCus),
                                              ceil_div(longest, kLinMaxSplits)});
     if (2 * longest > 3 * share) len = share;
   }
@@ -402,8 +407,8 @@ LinJob lin_job(const LinShape& s, int j, const AnyOperand& a, const AnyOperand& 
   r.steps = (int32_t)ceil_div(a.k, kAnyBK);
   r.splits = s.splits[j];
   r.split_steps = (int32_t)ceil_div(std::max(r.steps, 1), r.splits);
-  r.tiles_m = (int32_t)ceil_div(r.m, s.tile);
-  r.tiles_n = (int32_t)ceil_div(r.n, s.tile);
+  r.tiles_m = (int32_t)ceil_div(r.m, s.tile_m);
+  r.tiles_n = (int32_t)ceil_div(r.n, s.tile_n);
   r.items = r.tiles_m * r.tiles_n * r.splits;
   r.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + s.partial_off[j]);
   return r;
@@ -606,8 +611,8 @@ extern "C" ovl_status gemm_epilogue_run(const gemm_epilogue_desc* desc, const vo
   args.job[0] = lin_job(s, 0, {static_cast<const uint16_t*>(a), d.lda, d.m, d.k},
                         {static_cast<const uint16_t*>(b), d.ldb, d.n, d.k}, e, workspace);
   args.sum.splits = 1;
-  if (s.deep) return lin_fwd_launch<Fwd128D>(args, stream);
-  return s.tile == 256 ? lin_fwd_launch<Fwd256>(args, stream) : lin_fwd_launch<Fwd128>(args, stream);
+  if (s.tile_m == 64) return lin_fwd_launch<Fwd64>(args, stream);
+  return s.tile_m == 256 ? lin_fwd_launch<Fwd256>(args, stream) : lin_fwd_launch<Fwd128>(args, stream);
 }
 
 extern "C" size_t gemm_epilogue_grad_workspace_bytes(const gemm_epilogue_grad_desc* desc) {
@@ -683,6 +688,6 @@ extern "C" ovl_status gemm_epilogue_grad_run(const gemm_epilogue_grad_desc* desc
     u.strips = (int32_t)ceil_div(d.n, 64);
     u.items = u.strips * u.splits;
   }
-  if (s.deep) return lin_grad_launch<Db128D, Da128D>(args, stream);
-  return s.tile == 256 ? lin_grad_launch<Db256, Da256>(args, stream) : lin_grad_launch<Db128, Da128>(args, stream);
+  if (s.tile_m == 64) return lin_grad_launch<Db64, Da64>(args, stream);
+  return s.tile_m == 256 ? lin_grad_launch<Db256, Da256>(args, stream) : lin_grad_launch<Db128, Da128>(args, stream);
 }
