@@ -17,7 +17,14 @@
 // each range backwards with the same grid, so that it begins with what the
 // first read last, which the caches still hold.  What a single workgroup can
 // hold goes through one launch.
+//
+// The table lies in the caller's workspace between upload and run, and its
+// entries are addresses: every entry carries a tag made of its contents, its
+// number and its plan's, and a wavefront that meets one whose tag is wrong
+// (never uploaded, another plan's, written over since) touches nothing that
+// it names.  The run then reports EINVAL, gives a NaN norm and scales nothing.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -30,15 +37,23 @@ namespace ovl {
 namespace {
 
 constexpr int kGcMaxGroups = 2048;  // workgroups of a launch, and float64 sums in the workspace
-constexpr int kGcUpload = 100;      // table entries that travel as one launch's arguments
+constexpr int kGcUpload = 80;       // table entries that travel as one launch's arguments
 constexpr size_t kGcSums = kCounterBytes;
 constexpr size_t kGcTable = kGcSums + kGcMaxGroups * sizeof(double);
 
 struct GcEntry {
   uint64_t src, dst;  // dst 0: the tensor only counts in the norm
-  int64_t first;      // number of its first slot
+  int64_t first, end; // its slots
   int64_t count;      // 2 * elements + (1 for float32, 0 for bf16)
+  uint64_t tag;
 };
+
+// Few instructions: a launch of a few microseconds also waits for its code.
+// plan: random bits of the entry's plan.
+__host__ __device__ inline uint64_t gc_tag(const GcEntry& e, int64_t i, uint64_t plan) {
+  return (e.src + (e.dst << 1) + ((uint64_t)e.first << 2) + ((uint64_t)e.end << 3) + ((uint64_t)e.count << 4) +
+          (uint64_t)i) ^ plan;
+}
 
 struct GcUpload {
   GcEntry e[kGcUpload];
@@ -47,7 +62,9 @@ struct GcUpload {
 };
 
 struct GcArgs {
-  const GcEntry* table;  // tensors + 1 entries; the last holds the number of slots
+  const GcEntry* table;
+  ErrRec* err;
+  uint64_t plan;
   double* sums;
   float* norm;
   int64_t tensors, slots;
@@ -94,18 +111,30 @@ __device__ inline u32x4 gc_scaled(u32x4 v, bool f32, float coef) {
   return v;
 }
 
-// The last tensor whose first slot is <= v (the one that holds slot v:
-// tensors without slots share their first slot with the one behind them).
-__device__ inline int64_t gc_find(const GcEntry* table, int64_t tensors, int64_t v) {
+__device__ inline uint64_t gc_lane(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
+
+// The last tensor whose first slot is <= v, the one that holds slot v, and its
+// number.  The last round's lanes hold the entries that they look at, so that
+// the one found needs no load of its own.
+__device__ inline GcEntry gc_find(const GcEntry* table, int64_t tensors, int64_t v, int64_t& at) {
   int64_t lo = 0, n = tensors;
-  while (n > 1) {
+  while (n > 64) {
     const int64_t step = (n + 63) / 64, i = lane_id() * step;
     const bool le = i < n && table[lo + i].first <= v;
-    const int below = __popcll(__ballot(le));  // >= 1: table[lo].first <= v
+    // At least 1 in a sound table, and in any other: lo stays an entry's number.
+    const int below = max(1, (int)__popcll(__ballot(le)));
     lo += (below - 1) * step;
     n = min(step, n - (below - 1) * step);
   }
-  return lo;
+  const GcEntry e = table[lo + min((int64_t)lane_id(), n - 1)];
+  const int pick = uniform(max(1, (int)__popcll(__ballot(lane_id() < n && e.first <= v))) - 1);
+  at = uniform64(lo + pick);
+  return GcEntry{gc_lane(e.src, pick),           gc_lane(e.dst, pick),
+                 (int64_t)gc_lane(e.first, pick), (int64_t)gc_lane(e.end, pick),
+                 (int64_t)gc_lane(e.count, pick), gc_lane(e.tag, pick)};
 }
 
 // One tensor's slots, seen from the wavefront.
@@ -115,12 +144,11 @@ struct GcTensor {
   bool f32;
   int head;  // bytes of slot 0 ahead of the tensor
 
-  __device__ GcTensor(const GcEntry* table, int64_t t) {
-    const GcEntry e = table[t];
+  __device__ GcTensor(const GcEntry& e) {
     src = e.src;
     dst = e.dst;
     first = e.first;
-    slots = table[t + 1].first - e.first;
+    slots = e.end - e.first;
     count = e.count >> 1;
     f32 = e.count & 1;
     head = (int)(src & 15);
@@ -149,13 +177,23 @@ struct GcTensor {
 
 constexpr int kGcU = 4;  // 16-byte loads in flight per lane
 
-// Sum of squares over slots [v0, v1), this lane's share.
+// Sum of squares over slots [v0, v1), this lane's share; minus infinity where
+// the table is not this plan's.  (Sound entries follow each other without a
+// gap up to the last slot, so a walk from the one that holds v0 stays in the
+// table.  Every entry holds slots, so that the launch looks at all of them.)
 __device__ inline double gc_sum_range(const GcArgs& a, int64_t v0, int64_t v1) {
   double s = 0;
   if (v0 >= v1) return s;
   const int lane = lane_id();
-  for (int64_t t = uniform64(gc_find(a.table, a.tensors, v0)); v0 < v1; ++t) {
-    const GcTensor g(a.table, t);
+  int64_t t;
+  GcEntry entry = gc_find(a.table, a.tensors, v0, t);
+  for (;;) {
+    const uint64_t tag = gc_tag(entry, t, a.plan);
+    if (entry.tag != tag || v0 < entry.first || v0 >= entry.end) {
+      if (lane == 0) report_error(a.err, OVL_EINVAL, kSiteClip, t, (int64_t)entry.tag, (int64_t)tag);
+      return -HUGE_VAL;
+    }
+    const GcTensor g(entry);
     const int64_t b = v0 - g.first, e = min(v1 - g.first, g.slots);
     const int64_t w0 = max(b, g.whole0()), w1 = min(e, g.whole1());
     if (b < g.whole0() && b < e) {
@@ -179,6 +217,8 @@ __device__ inline double gc_sum_range(const GcArgs& a, int64_t v0, int64_t v1) {
       s += d * d;
     }
     v0 = g.first + e;
+    if (v0 >= v1) break;
+    entry = a.table[++t];
   }
   return s;
 }
@@ -202,38 +242,45 @@ __device__ inline void gc_scale_slot(const GcTensor& g, int64_t i, u32x4 v, floa
 }
 
 // dst = src * coef over slots [v0, v1), from the last to the first.  Both
-// streams are nontemporal, so that the stores do not push what the first pass
-// left in the caches out before it is read again (1 GiB of gradients, both
-// launches: 590 -> 553 us; 32 MiB: 19.2 -> 18.1).
+// streams are nontemporal (384M elements, both launches: 590 -> 553 us, of
+// which 44 in the next call's first launch, behind ordinary stores; 32 MiB:
+// 19.2 -> 18.1, in the second launch, which finds more of the first's reads).
+__device__ inline void gc_scale_tensor(const GcTensor& g, int64_t b, int64_t e, float coef) {
+  // In place with coef 1 nothing changes.
+  if (!g.dst || (g.dst == g.src && coef == 1.f)) return;
+  const int lane = lane_id();
+  const bool vec = ((g.dst ^ g.src) & 15) == 0;
+  const int64_t w0 = max(b, g.whole0()), w1 = min(e, g.whole1());
+  if (e > g.whole1() && e - 1 >= g.whole0()) {
+    const int64_t j = g.edge(e - 1);
+    if (j >= 0) g.store(j, g.load(j) * coef);
+  }
+  const u32x4* p = g.vec();
+  int64_t i = w1 - 1 - lane;
+  for (; i - (kGcU - 1) * 64 >= w0; i -= kGcU * 64) {
+    u32x4 v[kGcU];
+#pragma unroll
+    for (int u = 0; u < kGcU; ++u) v[u] = __builtin_nontemporal_load(p + i - u * 64);
+#pragma unroll
+    for (int u = 0; u < kGcU; ++u) gc_scale_slot(g, i - u * 64, v[u], coef, vec);
+  }
+  for (; i >= w0; i -= 64) gc_scale_slot(g, i, p[i], coef, vec);
+  if (b < g.whole0()) {
+    const int64_t j = g.edge(b);
+    if (j >= 0) g.store(j, g.load(j) * coef);
+  }
+}
+
 __device__ inline void gc_scale_range(const GcArgs& a, int64_t v0, int64_t v1, float coef) {
   if (v0 >= v1) return;
-  const int lane = lane_id();
-  for (int64_t t = uniform64(gc_find(a.table, a.tensors, v1 - 1)); v0 < v1; --t) {
-    const GcTensor g(a.table, t);
-    const int64_t b = max(v0 - g.first, (int64_t)0), e = v1 - g.first;
-    v1 = min(v1, g.first);
-    // In place with coef 1 nothing changes.
-    if (b >= e || !g.dst || (g.dst == g.src && coef == 1.f)) continue;
-    const bool vec = ((g.dst ^ g.src) & 15) == 0;
-    const int64_t w0 = max(b, g.whole0()), w1 = min(e, g.whole1());
-    if (e > g.whole1() && e - 1 >= g.whole0()) {
-      const int64_t j = g.edge(e - 1);
-      if (j >= 0) g.store(j, g.load(j) * coef);
-    }
-    const u32x4* p = g.vec();
-    int64_t i = w1 - 1 - lane;
-    for (; i - (kGcU - 1) * 64 >= w0; i -= kGcU * 64) {
-      u32x4 v[kGcU];
-#pragma unroll
-      for (int u = 0; u < kGcU; ++u) v[u] = __builtin_nontemporal_load(p + i - u * 64);
-#pragma unroll
-      for (int u = 0; u < kGcU; ++u) gc_scale_slot(g, i - u * 64, v[u], coef, vec);
-    }
-    for (; i >= w0; i -= 64) gc_scale_slot(g, i, p[i], coef, vec);
-    if (b < g.whole0()) {
-      const int64_t j = g.edge(b);
-      if (j >= 0) g.store(j, g.load(j) * coef);
-    }
+  int64_t t;
+  GcEntry entry = gc_find(a.table, a.tensors, v1 - 1, t);
+  for (;;) {
+    const GcTensor g(entry);
+    gc_scale_tensor(g, max(v0 - g.first, (int64_t)0), v1 - g.first, coef);
+    v1 = g.first;
+    if (v0 >= v1) break;
+    entry = a.table[--t];
   }
 }
 
@@ -256,7 +303,7 @@ __device__ inline double gc_group_sum(double s, double* lds) {
 }
 
 __device__ inline float gc_coef(const GcArgs& a, double sum, bool first) {
-  const double norm = sqrt(sum);
+  const double norm = sqrt(sum);  // NaN for a sum below 0
   if (first) *a.norm = (float)norm;
   const double c = (double)a.max_norm / (norm + 1e-6);
   return c >= 1.0 || isinf(a.max_norm) ? 1.f : (float)c;  // a NaN norm gives a NaN coefficient
@@ -276,6 +323,7 @@ __global__ __launch_bounds__(kThreads) void gc_scale_kernel(GcArgs a) {
   for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) s += a.sums[i];
   s = gc_group_sum<kThreads>(s, lds);
   const float coef = gc_coef(a, s, blockIdx.x == 0 && threadIdx.x == 0);
+  if (s < 0) return;  // not this plan's table
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 64) + uniform(threadIdx.x >> 6);
   const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
   gc_scale_range(a, v0, v1, coef);
@@ -288,7 +336,9 @@ __global__ __launch_bounds__(kGcOneThreads) void gc_one_kernel(GcArgs a) {
   const int64_t w = uniform(threadIdx.x >> 6);
   const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
   const double s = gc_group_sum<kGcOneThreads>(gc_sum_range(a, v0, v1), lds);
-  gc_scale_range(a, v0, v1, gc_coef(a, s, threadIdx.x == 0));
+  const float coef = gc_coef(a, s, threadIdx.x == 0);
+  if (s < 0) return;
+  gc_scale_range(a, v0, v1, coef);
 }
 
 }  // namespace
@@ -298,8 +348,12 @@ __global__ __launch_bounds__(kGcOneThreads) void gc_one_kernel(GcArgs a) {
 using namespace ovl;
 
 struct grad_clip_plan_s {
-  std::vector<GcEntry> table;  // tensors + 1
+  std::vector<GcEntry> table;
+  int64_t slots;
+  uint64_t id;  // 64 bits that no other plan of this process has
 };
+
+static std::atomic<uint64_t> gc_plans{0};
 
 extern "C" ovl_status grad_clip_plan(const grad_clip_tensor* tensors, int64_t num, grad_clip_plan_t* out) {
   if (!out) return OVL_EINVAL;
@@ -314,7 +368,7 @@ extern "C" ovl_status grad_clip_plan(const grad_clip_tensor* tensors, int64_t nu
     };
     std::vector<GcEntry> table;
     std::vector<Span> spans;
-    table.reserve(num + 1);
+    table.reserve(num);
     int64_t slot = 0;
     for (int64_t i = 0; i < num; ++i) {
       const grad_clip_tensor& t = tensors[i];
@@ -325,13 +379,13 @@ extern "C" ovl_status grad_clip_plan(const grad_clip_tensor* tensors, int64_t nu
       const uint64_t size = t.type == OVL_F32 ? 4 : 2, bytes = (uint64_t)t.count * size;
       if (t.count && !src) return OVL_EINVAL;
       if ((src | dst) & (size - 1)) return OVL_EALIGN;
-      table.push_back({src, dst, slot, 2 * t.count + (t.type == OVL_F32)});
       if (!t.count) continue;
+      const int64_t first = slot;
       slot += (int64_t)(((src & 15) + bytes + 15) / 16);
+      table.push_back({src, dst, first, slot, 2 * t.count + (t.type == OVL_F32), 0});
       if (dst != src) spans.push_back({src, src + bytes, i, false});
       if (dst) spans.push_back({dst, dst + bytes, i, true});
     }
-    table.push_back({0, 0, slot, 0});
     // What is written may overlap nothing else that the call reads or writes
     // (a tensor clipped in place is one span).
     std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.lo < y.lo; });
@@ -342,6 +396,9 @@ extern "C" ovl_status grad_clip_plan(const grad_clip_tensor* tensors, int64_t nu
       if (s.written) end_written = std::max(end_written, s.hi);
     }
     grad_clip_plan_s* p = new grad_clip_plan_s;
+    p->slots = slot;
+    p->id = (++gc_plans + 1) * 0x9E3779B97F4A7C15ull;  // odd: a bijection of the plan's number
+    for (size_t i = 0; i < table.size(); ++i) table[i].tag = gc_tag(table[i], (int64_t)i, p->id);
     p->table.swap(table);
     *out = p;
   } catch (const std::bad_alloc&) {
@@ -385,9 +442,11 @@ extern "C" ovl_status grad_norm_clip_run(grad_clip_plan_t p, float max_norm, flo
   GcArgs a = {};
   a.table = reinterpret_cast<const GcEntry*>(static_cast<uint8_t*>(workspace) + kGcTable);
   a.sums = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + kGcSums);
+  a.err = static_cast<ErrRec*>(workspace);
+  a.plan = p->id;
   a.norm = norm;
-  a.tensors = (int64_t)p->table.size() - 1;
-  a.slots = p->table.back().first;
+  a.tensors = (int64_t)p->table.size();
+  a.slots = p->slots;
   a.max_norm = max_norm;
   if (a.slots <= 8192) {
     a.per_wave = ceil_div(a.slots, kGcOneThreads / 64);

@@ -604,10 +604,15 @@ class GradClipPlan:
                                     buf(f"output {i}", d, s.element_size(), 1, n) or None, n,
                                     F32 if s.dtype == torch.float32 else BF16, 0)
         self.tensors = (src, dst)
+        self.device = buf.device
         h = c_void_p()
         _check(lib().grad_clip_plan(arr, len(src), byref(h)), "grad_clip_plan", True)
         self.handle = h
         self.workspace_bytes = lib().grad_clip_workspace_bytes(h)
+
+    def _here(self, buf):
+        if buf.device != self.device:
+            buf.refuse("plan", "is of tensors on another device than the current one")
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -622,6 +627,7 @@ def grad_clip_plan(src, dst=None) -> GradClipPlan:
 
 def grad_clip_upload(plan: GradClipPlan, workspace, stream=None, raise_on_error: bool = True) -> int:
     buf = _Buffers("grad_clip_upload")
+    plan._here(buf)
     ws = buf("workspace", workspace, 1, 1, plan.workspace_bytes)
     return _check(lib().grad_clip_upload(plan.handle, ws, _stream(stream)), "grad_clip_upload", raise_on_error)
 
@@ -630,6 +636,7 @@ def grad_norm_clip_run(plan: GradClipPlan, max_norm: float, norm, workspace, str
                        raise_on_error: bool = True) -> int:
     """norm (float32 [1]) = the global norm; every dst = src * min(1, max_norm / (norm + 1e-6))."""
     buf = _Buffers("grad_norm_clip_run")
+    plan._here(buf)
     st = lib().grad_norm_clip_run(plan.handle, max_norm, buf("norm", norm, 4, 1, 1),
                                   buf("workspace", workspace, 1, 1, plan.workspace_bytes), _stream(stream))
     return _check(st, "grad_norm_clip_run", raise_on_error)

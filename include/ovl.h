@@ -504,9 +504,11 @@ ovl_status ring_allreduce_run(const ring_desc* desc, const float* const* in, flo
  * These calls use no flags and no epochs: each is complete in stream order.
  * Their workspaces need no reset between calls (each call says whether it
  * needs one before the first) and may be shared by any calls that do not
- * overlap in time, captured ones included.  Row strides (ld*) count elements, 0 standing for a
- * dense row; they are multiples of 8, at most 2^20, and what lies between a
- * row's end and the next row is neither read nor written.  Outputs may not
+ * overlap in time, captured ones included; only the clipping's holds
+ * something from call to call (its plan's table, see there).  Row strides
+ * (ld*) count elements, 0 standing for a dense row; they are multiples of 8,
+ * at most 2^20, and what lies between a row's end and the next row is neither
+ * read nor written.  Outputs may not
  * overlap inputs, but for the cases named at each call.
  * ---------------------------------------------------------------------- */
 enum { OVL_BF16 = 0, OVL_F32 = 1, OVL_FP8 = 2 /* E4M3 codes with scales */ };
@@ -661,7 +663,11 @@ size_t grad_clip_workspace_bytes(grad_clip_plan_t plan);
 
 /* Writes the plan's table into `workspace` (kernels on `stream`, which carry
  * the entries in their arguments); once for any number of runs of this plan
- * on this workspace, ordered before them. */
+ * on this workspace, ordered before them.  A call of another kind on the same
+ * workspace, or an upload of another plan, writes over it: upload again.  A
+ * run that finds a table that is not its plan's reports EINVAL to ovl_check
+ * (for which the workspace is zeroed once, before its first upload), sets
+ * norm to NaN and scales nothing. */
 ovl_status grad_clip_upload(grad_clip_plan_t plan, void* workspace, hipStream_t stream);
 
 /* norm: device float32.  max_norm >= 0, infinite for the norm alone (a dst

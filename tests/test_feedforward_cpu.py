@@ -199,3 +199,13 @@ def test_binding_refuses_host_and_short_tensors():
         o.grad_clip_plan([torch.zeros(4)])
     with pytest.raises(o.OvlError):
         o.grad_clip_plan([torch.zeros(4)], [])
+
+
+def test_binding_refuses_a_plan_of_another_device():
+    o = ovl()
+    p = o.grad_clip_plan([])
+    p.device = 5
+    for call in (lambda: o.grad_clip_upload(p, P, stream=0), lambda: o.grad_norm_clip_run(p, 1.0, P, P, stream=0)):
+        with pytest.raises(o.OvlError) as e:
+            call()
+        assert e.value.status == o.OVL_EINVAL

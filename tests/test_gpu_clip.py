@@ -172,3 +172,41 @@ def test_one_plan_many_runs_capture_and_new_values():
         first = [d.clone() for d in dst]
         o.grad_norm_clip_run(plan, 0.5, norm, ws)
         assert all(t.equal(a, b) for a, b in zip(first, dst))
+
+
+@pytest.mark.parametrize("sizes", [[50, 7], [70000, 31, 0, 40000]])
+@pytest.mark.parametrize("how", ["never uploaded", "another plan's", "another call's", "one entry"])
+def test_a_table_that_is_not_the_plan_s_is_refused(sizes, how):
+    """Nothing that such a table names is read or written: EINVAL, a NaN norm,
+    gradients as they were; after an upload the run is whole."""
+    o, t = ovl(), fu.torch()
+    src = tensors(sizes)
+    kept = [v.clone() for v in src]
+    plan = o.grad_clip_plan(src)
+    d = o.gemm_epilogue_desc(8, 4096, 4096)
+    ws = fu.workspace(max(plan.workspace_bytes, o.gemm_epilogue_workspace_bytes(d)))
+    if how == "another plan's":
+        other = [v.clone() for v in src]
+        o.grad_clip_upload(o.grad_clip_plan(other), ws)
+    elif how != "never uploaded":
+        o.grad_clip_upload(plan, ws)
+        if how == "another call's":
+            out = t.empty(8, 4096, dtype=t.bfloat16, device="cuda")
+            o.gemm_epilogue_run(d, fu.normal(1, 8, 4096), fu.normal(2, 4096, 4096), None, None, out, None, ws)
+        else:  # the first entry's number of elements
+            words = ws[:plan.workspace_bytes // 8 * 8].view(t.int64)
+            at = (words == src[0].data_ptr()).nonzero()
+            assert at.shape[0] == 2  # src and dst of the entry
+            words[int(at[0]) + 4] += 2
+    norm = t.full((1,), -1.0, device="cuda")
+    say(f"  grad_norm_clip_run on a table: {how}")
+    o.grad_norm_clip_run(plan, 0.25, norm, ws)
+    st, detail = o.ovl_check(ws, raise_on_error=False)
+    assert st == o.OVL_EINVAL
+    assert math.isnan(float(norm))
+    assert all(t.equal(a, b) for a, b in zip(src, kept))
+    o.ovl_flags_reset(None, 0, ws, ws.numel())
+    o.grad_clip_upload(plan, ws)
+    o.grad_norm_clip_run(plan, 0.25, norm, ws)
+    assert o.ovl_check(ws, raise_on_error=False)[0] == o.OVL_OK
+    check([fu.f64(v) for v in kept], src, float(norm), 0.25)
