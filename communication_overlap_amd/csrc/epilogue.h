@@ -123,8 +123,8 @@ __device__ inline void store8(const float (&v)[8], void* p, int64_t i, int type)
 
 // The epilogue of one product, columns n (a multiple of 8):
 //   z = sum + bias;  out = act(z) + residual;  z_out = bf16(z)
-// or, with z_in, out = sum * act'(z_in) (the gradient's), or with `add` a
-// float addend in out's type: out = sum + add.
+// or, with z_in, out = sum * act'(z_in) (the gradient's).  A gradient's db_in is
+// its residual.
 struct Epilogue {
   void* out;
   void* z_out;           // bf16, or null

@@ -1,19 +1,26 @@
 // A whole mixture-of-experts layer for a few tokens: routing, the experts'
 // two products, the gate-weighted sum.  What it must read is the chosen
 // experts' weights; everything else is small, so the experts' products are
-// rows.h's streams, spread over the chip by (chosen expert, 64 columns,
-// range of k), and every reduction is done by whichever workgroup arrives
-// last, in a fixed order.
-//  1. Routing (with a router): ranges of hidden x groups of 4 tokens, sums
-//     in float64 so that a choice between two near logits does not hang on
-//     the order of a sum; the last range of a token group picks.
+// rows.h's streams, spread over the chip by (chosen expert, columns, range of
+// k), a workgroup a compute unit taking items in turn.  Partial sums meet in a
+// fixed order, at whichever workgroup arrives last or in a launch of their own.
+//  1. Routing (with a router), two launches: logits of ranges of hidden x
+//     groups of 4 tokens, in float64 so that a choice between two near logits
+//     does not hang on the order of a sum; then each token's ranges added up
+//     and its experts picked.  (One launch, the last range picking, took 0.4 us
+//     more for a token and 5 more for 64.)
 //  2. Up: u = x w1, then h = act(gate) * up as bf16 planes (see ovl.h).
-//  3. Down: h w2 per (token, choice) pair in float32; the last workgroup of a
-//     column tile, over all experts and ranges, sums each token's choices
-//     with their gates, in order, and stores out.
-// Every workgroup of 2 and 3 finds its expert itself: the chosen ids are at
-// most 1024 words, from which it takes the set of distinct experts and its
-// own expert's pairs.
+//  3. Down: h w2 per (token, choice) pair in float32, and the sum of each
+//     token's choices with their gates, in order: by the last workgroup of a
+//     column tile, over all experts and ranges, for at most 8 tokens in few
+//     tiles, else by a launch of its own.
+// Every workgroup of 2 and 3 lists the distinct experts itself, from the at
+// most 1024 chosen ids, and finds its items' pairs there.
+//
+// Measured (4096 x 1408, 64 experts, gated): one token, top 2, bf16 35 us, of
+// which 12 is the 70 MB stream and the rest the four launches' starts and ends;
+// 64 tokens, top 2, bf16 343 us (HBM: 1.85 GB, up 5.6 and down 5.4 TB/s); 9
+// tokens, top 4, FP8 101 us (HBM: 437 MB, up 4.8 and down 3.9 TB/s).
 #include <algorithm>
 
 #include "epilogue.h"
@@ -724,6 +731,7 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
       !aligned16(out) || !aligned16(router) || (reinterpret_cast<uintptr_t>(topk_idx) & 3u) ||
       (reinterpret_cast<uintptr_t>(gates) & 3u))
     return OVL_EALIGN;
+  if (out == x || out == w1 || out == w2) return OVL_EINVAL;
   const MoeShape s = moe_shape(*d);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeArgs a = {};

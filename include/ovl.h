@@ -508,8 +508,9 @@ ovl_status ring_allreduce_run(const ring_desc* desc, const float* const* in, flo
  * something from call to call (its plan's table, see there).  Row strides
  * (ld*) count elements, 0 standing for a dense row; they are multiples of 8,
  * at most 2^20, and what lies between a row's end and the next row is neither
- * read nor written.  Outputs may not
- * overlap inputs, but for the cases named at each call.
+ * read nor written.  Outputs may not overlap inputs or each other, but for the
+ * cases named at each call; one that begins where another such buffer does is
+ * refused (EINVAL).
  * ---------------------------------------------------------------------- */
 enum { OVL_BF16 = 0, OVL_F32 = 1, OVL_FP8 = 2 /* E4M3 codes with scales */ };
 
@@ -576,7 +577,7 @@ size_t gemm_epilogue_grad_workspace_bytes(const gemm_epilogue_grad_desc* desc);
  * NONE and da is asked for (else NULL).  da, db, dbias: each may be NULL (not
  * computed); db_in [k][n] of db_type and dbias_in [n] may be NULL (nothing to
  * add) or the outputs themselves (accumulation in place; strides as db's).
- * dz may be dy, and da may be z_in (bf16, equal strides).  With m = 0 db and dbias are
+ * dz may be dy or z, and da may be z_in (bf16, equal strides).  With m = 0 db and dbias are
  * db_in and dbias_in, or zero, and the row buffers may be NULL.
  * workspace: gemm_epilogue_grad_workspace_bytes(desc) bytes, no reset needed.
  * Errors as for gemm_epilogue_run (operands: a, b, dz). */
@@ -599,7 +600,8 @@ ovl_status gemm_epilogue_grad_run(const gemm_epilogue_grad_desc* desc, const voi
  * outside [0, experts) (an expert of another rank) contribute nothing, and an
  * id may stand more than once.  Sums and h are float32 (h enters the matrix
  * units as two bf16 terms, 16 bits, for bf16 output and three, 24 bits, for
- * float32); out is rounded once.  The same call gives the same bits every
+ * float32, so an infinite weight in w2 makes its column NaN); out is rounded
+ * once.  The same call gives the same bits every
  * time; how k is cut into ranges, and with it the last bits of a token's
  * row, goes by how many distinct experts the call's tokens chose.
  * ---------------------------------------------------------------------- */

@@ -209,3 +209,35 @@ def test_binding_refuses_a_plan_of_another_device():
         with pytest.raises(o.OvlError) as e:
             call()
         assert e.value.status == o.OVL_EINVAL
+
+
+Q = [4096 * i for i in range(2, 16)]  # distinct aligned addresses that nothing dereferences
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=Q[0]), dict(out=Q[1]), dict(z=Q[0]), dict(z=Q[1]), dict(z=Q[3]),      # over an input or another output
+    dict(residual=Q[5], z=Q[5]),
+    dict(residual=Q[3], res_type="f32"), dict(residual=Q[3], ldr=24),               # in place of another type or stride
+])
+def test_gemm_epilogue_refuses_overlaps(kw):
+    o = ovl()
+    assert linear(o, **{**dict(a=Q[0], b=Q[1], out=Q[3], ws=Q[4]), **kw})[0] == o.OVL_EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dz=Q[1], lddy=24), dict(dz=Q[1], dy_type="f32"), dict(dz=Q[2], ldz=24),    # dz over dy or z
+    dict(da=Q[6], da_type="f32"), dict(da=Q[6], ldda=32),                           # da over z_in
+    dict(da=Q[3]), dict(da=Q[4]), dict(da=Q[5]), dict(db=Q[3]), dict(db=Q[4]), dict(dbias=Q[4]),
+    dict(dz=Q[4]), dict(dz=Q[5]), dict(da=Q[8]), dict(da=Q[9], db_in=Q[9]),
+])
+def test_gemm_epilogue_grad_refuses_overlaps(kw):
+    o = ovl()
+    base = dict(dy=Q[1], z=Q[2], dz=Q[3], a=Q[4], b=Q[5], z_in=Q[6], da=Q[7], db=Q[8], dbias=Q[10], ws=Q[11],
+                act="silu", act_in="relu")
+    assert grad(o, **{**base, **kw})[0] == o.OVL_EINVAL
+
+
+def test_moe_layer_refuses_overlaps():
+    o = ovl()
+    for out in Q[:3]:
+        assert moe(o, x=Q[0], w1=Q[1], w2=Q[2], out=out, router=Q[4], topk=Q[5], gates=Q[6], ws=Q[7])[0] == o.OVL_EINVAL

@@ -363,3 +363,12 @@ def test_grad_against_differences(act):
         up[at], dn[at] = x[at] + h * d, x[at] - h * d
         step = np.abs(x[0]) @ np.abs(d) if at == 1 else (np.abs(d) @ np.abs(x[1]) if at == 0 else np.abs(d)[None, :])
         assert abs((loss(up) - loss(dn)) / (2 * h) - float((fu.f64(g) * d).sum())) <= float((slack * step).sum()) + 1e-4
+
+
+def test_grad_dz_over_z():
+    t = fu.torch()
+    w, c = (Grad(90, 72, 64, "silu", act="relu", seed=12) for _ in range(2))
+    w.run()
+    c.dz = c.z
+    c.run()
+    assert t.equal(c.dz, w.dz) and t.equal(c.da, w.da) and t.equal(c.db, w.db)
