@@ -19,7 +19,7 @@
 // hold goes through one launch.
 //
 // Measured, with what bounds them: 384M elements in 60 tensors 555 us (HBM:
-// 6.2 TB/s reading, then 5.3 reading and writing); 8M float32 17.8 us (the
+// 6.2 TB/s reading, then 5.3 reading and writing); 8M float32 17.6 us (the
 // second launch's start, which adds up 1024 sums and searches the table, and
 // memory); 8 tensors, 4099 elements, 6.1 us (one launch: a search, two
 // rounds of loads, a barrier between them).
@@ -277,10 +277,8 @@ __device__ inline void gc_scale_tensor(const GcTensor& g, int64_t b, int64_t e, 
   }
 }
 
-__device__ inline void gc_scale_range(const GcArgs& a, int64_t v0, int64_t v1, float coef) {
+__device__ inline void gc_scale_range(const GcArgs& a, int64_t v0, int64_t v1, GcEntry entry, int64_t t, float coef) {
   if (v0 >= v1) return;
-  int64_t t;
-  GcEntry entry = gc_find(a.table, a.tensors, v1 - 1, t);
   for (;;) {
     const GcTensor g(entry);
     gc_scale_tensor(g, max(v0 - g.first, (int64_t)0), v1 - g.first, coef);
@@ -325,14 +323,17 @@ __global__ __launch_bounds__(kThreads) void gc_norm_kernel(GcArgs a) {
 
 __global__ __launch_bounds__(kThreads) void gc_scale_kernel(GcArgs a) {
   __shared__ double lds[kThreads / 64];
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 64) + uniform(threadIdx.x >> 6);
+  const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
   double s = 0;
   for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) s += a.sums[i];
+  // (The search's loads are on their way with the sums'.)
+  int64_t t = 0;
+  GcEntry entry = gc_find(a.table, a.tensors, max(v1 - 1, (int64_t)0), t);
   s = gc_group_sum<kThreads>(s, lds);
   const float coef = gc_coef(a, s, blockIdx.x == 0 && threadIdx.x == 0);
   if (s < 0) return;  // not this plan's table
-  const int64_t w = (int64_t)blockIdx.x * (kThreads / 64) + uniform(threadIdx.x >> 6);
-  const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
-  gc_scale_range(a, v0, v1, coef);
+  gc_scale_range(a, v0, v1, entry, t, coef);
 }
 
 constexpr int kGcOneThreads = 1024;
@@ -343,8 +344,10 @@ __global__ __launch_bounds__(kGcOneThreads) void gc_one_kernel(GcArgs a) {
   const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
   const double s = gc_group_sum<kGcOneThreads>(gc_sum_range(a, v0, v1), lds);
   const float coef = gc_coef(a, s, threadIdx.x == 0);
-  if (s < 0) return;
-  gc_scale_range(a, v0, v1, coef);
+  if (s < 0 || v0 >= v1) return;
+  int64_t t;
+  const GcEntry entry = gc_find(a.table, a.tensors, v1 - 1, t);
+  gc_scale_range(a, v0, v1, entry, t, coef);
 }
 
 }  // namespace
