@@ -8,7 +8,9 @@
 //     groups of 4 tokens, in float64 so that a choice between two near logits
 //     does not hang on the order of a sum; then each token's ranges added up
 //     and its experts picked.  (One launch, the last range picking, took 0.4 us
-//     more for a token and 5 more for 64.)
+//     more for a token and 5 more for 64.)  One token's experts every workgroup
+//     of 2 picks for itself (33.4 us for the layer, 34.5 with the launch): it
+//     reads at most 64 logits a range, from its die's cache.
 //  2. Up: u = x w1, then h = act(gate) * up as bf16 planes (see ovl.h).
 //  3. Down: h w2 per (token, choice) pair in float32, and the sum of each
 //     token's choices with their gates, in order: by the last workgroup of a
@@ -17,8 +19,8 @@
 // Every workgroup of 2 and 3 lists the distinct experts itself, from the at
 // most 1024 chosen ids, and finds its items' pairs there.
 //
-// Measured (4096 x 1408, 64 experts, gated): one token, top 2, bf16 35 us, of
-// which 12 is the 70 MB stream and the rest the four launches' starts and ends;
+// Measured (4096 x 1408, 64 experts, gated): one token, top 2, bf16 33.4 us, of
+// which 12 is the 70 MB stream and the rest the three launches' starts and ends;
 // 64 tokens, top 2, bf16 343 us (HBM: 1.85 GB, up 5.6 and down 5.4 TB/s); 9
 // tokens, top 4, FP8 101 us (HBM: 437 MB, up 4.8 and down 3.9 TB/s).
 #include <algorithm>
@@ -60,6 +62,7 @@ struct MoeArgs {
   int32_t down_tiles, down_max, down_steps;
   int32_t chunks;
   int32_t fused;  // the down launch sums the choices itself
+  int32_t pick;   // the up launch picks the one token's experts itself
 };
 
 // ---------------------------------------------------------------- routing
@@ -80,10 +83,14 @@ __device__ inline double moe_wave_max(double v) {
   return v;
 }
 
-// Token t's choices from its logits in LDS, by one wavefront: the largest
+// A token's choices from its logits in LDS, by one wavefront: the largest
 // remaining one, topk times; among equals the lowest id, a NaN when nothing
-// else remains (fmax passes NaN over).
-__device__ inline void moe_pick(const MoeArgs& a, int t, const double* logits) {
+// else remains (fmax passes NaN over).  Lane j holds choice j and its gate.
+struct MoeChoice {
+  int32_t id;
+  float gate;
+};
+__device__ inline MoeChoice moe_pick(const MoeArgs& a, const double* logits) {
   const int lane = lane_id();
   double v[4];
   bool have[4];
@@ -134,10 +141,7 @@ __device__ inline void moe_pick(const MoeArgs& a, int t, const double* logits) {
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) chosen += __shfl_xor(chosen, d, 64);
   }
-  if (lane < a.topk_n) {
-    a.topk[t * a.topk_n + lane] = my_id;
-    a.gates[t * a.topk_n + lane] = mine / chosen;
-  }
+  return {my_id, mine / chosen};
 }
 
 // Workgroup (range of hidden, TT tokens): EP lanes across the experts, 256 /
@@ -184,13 +188,12 @@ __global__ __launch_bounds__(kThreads) void moe_logits_kernel(MoeArgs a) {
   }
 }
 
-// One token a workgroup: the ranges' sums, 256 / EP threads a logit, those in
-// order, and the choice.
+// Token t's logits into LDS [256 / EP][EP]: the ranges' sums, 256 / EP threads
+// a logit, those in order.
 template <int EP>
-__global__ __launch_bounds__(kThreads) void moe_pick_kernel(MoeArgs a) {
+__device__ inline void moe_logits(const MoeArgs& a, int t, double* part) {
   constexpr int R = kThreads / EP, U = 8;
-  __shared__ double part[R][EP];
-  const int t = blockIdx.x, e = threadIdx.x % EP, rr = threadIdx.x / EP;
+  const int e = threadIdx.x % EP, rr = threadIdx.x / EP;
   const double* p = a.logits + (int64_t)t * a.experts + min(e, a.experts - 1);
   const int64_t step = (int64_t)a.tokens * a.experts;
   double s = 0;
@@ -201,15 +204,28 @@ __global__ __launch_bounds__(kThreads) void moe_pick_kernel(MoeArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) s += c + u * R < a.chunks ? q[u] : 0.0;
   }
-  part[rr][e] = s;
+  part[rr * EP + e] = s;
   __syncthreads();
   if (rr == 0) {
 #pragma unroll
-    for (int q = 1; q < R; ++q) s += part[q][e];
-    part[0][e] = s;
+    for (int q = 1; q < R; ++q) s += part[q * EP + e];
+    part[e] = s;
   }
   __syncthreads();
-  if (threadIdx.x < 64) moe_pick(a, t, part[0]);
+}
+
+// One token a workgroup.
+template <int EP>
+__global__ __launch_bounds__(kThreads) void moe_pick_kernel(MoeArgs a) {
+  __shared__ double part[kThreads];
+  moe_logits<EP>(a, blockIdx.x, part);
+  if (threadIdx.x < 64) {
+    const MoeChoice c = moe_pick(a, part);
+    if (lane_id() < a.topk_n) {
+      a.topk[blockIdx.x * a.topk_n + lane_id()] = c.id;
+      a.gates[blockIdx.x * a.topk_n + lane_id()] = c.gate;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- experts
@@ -238,13 +254,13 @@ struct MoeScales {
 __device__ inline int32_t lds_word(const int32_t* p) { return *OVL_LDS(const int32_t, p); }
 
 // Reads the chosen ids and lists the distinct experts among them; returns how
-// many there are.
+// many there are.  id: this thread's choice of the only token, else null.
 template <int N>
-__device__ inline int moe_begin(const MoeArgs& a, MoeLds<N>& s) {
+__device__ inline int moe_begin(const MoeArgs& a, MoeLds<N>& s, const int32_t* id = nullptr) {
   if (threadIdx.x < 4) s.mask[threadIdx.x] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < a.pairs; i += kThreads) {
-    const int e = a.topk[i];
+    const int e = id ? *id : a.topk[i];
     const bool here = e >= 0 && e < a.experts;
     s.ids[i] = here ? e : -1;
     if (here) atomicOr(reinterpret_cast<unsigned long long*>(&s.mask[e >> 6]), 1ull << (e & 63));
@@ -439,7 +455,20 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a, int planes)
   __shared__ __align__(16) uint8_t sc[C::FP8 ? sizeof(MoeScales) : 16];
   MoeScales* scales = reinterpret_cast<MoeScales*>(sc);
   constexpr int PR = C::COLS / 8;  // pieces of a row
-  const int active = moe_begin(a, s);
+  int active;
+  if (a.pick) {
+    double* part = reinterpret_cast<double*>(moe_lds);
+    moe_logits<64>(a, 0, part);
+    MoeChoice c = {-1, 0.f};
+    if (threadIdx.x < 64) c = moe_pick(a, part);
+    if (blockIdx.x == 0 && (int)threadIdx.x < a.topk_n) {
+      a.topk[threadIdx.x] = c.id;
+      a.gates[threadIdx.x] = c.gate;
+    }
+    active = moe_begin(a, s, &c.id);
+  } else {
+    active = moe_begin(a, s);
+  }
   MoeGen<C, true> gen(a, s, scales, active);
   row_stream<C>(gen, moe_lds, [&](int32_t u, const float* st) {
     const int item = gen.c_item, sp = gen.range_of(item), tile = gen.tile(item);
@@ -671,6 +700,7 @@ ovl_status moe_route(const MoeArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((moe_logits_kernel<EP, kMoeRouteTokens>), dim3(a.chunks * ceil_div(a.tokens, kMoeRouteTokens)),
                        dim3(kThreads), 0, stream, a);
   OVL_HIP_TRY(hipGetLastError());
+  if (a.pick) return OVL_OK;
   hipLaunchKernelGGL((moe_pick_kernel<EP>), dim3(a.tokens), dim3(kThreads), 0, stream, a);
   OVL_HIP_TRY(hipGetLastError());
   return OVL_OK;
@@ -770,6 +800,7 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
   // At most one unit a workgroup, and no more tokens than one workgroup sums at
   // once (40 tokens of 112 columns: 22 us so, 12 with a launch for the sum).
   a.fused = (int64_t)s.pairs * s.down_tiles <= kMoeGroups && s.pairs <= 8 * d->topk;
+  a.pick = router && d->tokens == 1 && d->experts <= 64;
   if (router) {
     st = d->experts <= 64 ? moe_route<64>(a, stream)
                           : (d->experts <= 128 ? moe_route<128>(a, stream) : moe_route<256>(a, stream));

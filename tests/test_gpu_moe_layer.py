@@ -269,3 +269,31 @@ def test_same_bits_capture_and_a_shared_workspace(T, w):
         t.cuda.synchronize()
         assert t.equal(c.out, want)
         e.check()
+
+
+@pytest.mark.parametrize("H,E,K", [(64, 1, 1), (64, 9, 4), (4096, 64, 8), (4104, 64, 2), (72, 65, 3), (200, 256, 8)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_one_token_picks_as_a_row_of_many_does(H, E, K, norm):
+    """A token alone has a routing of its own; its choices and gates are those it
+    has beside others, ties and NaN among the logits included."""
+    t = fu.torch()
+    many, one = Moe(3, H, 16, E, K, norm=norm, seed=20), Moe(1, H, 16, E, K, norm=norm, seed=20)
+    for x in (many, one):
+        x.router = fu.normal(21, H, E, sigma=H ** -0.5)
+    one.x = many.x[1:2].clone()
+    for i in range(3):
+        if i == 1 and E > 4:     # ties, between near and far ids
+            for x in (many, one):
+                x.router[:, E - 1] = x.router[:, 0]
+                x.router[:, 3] = x.router[:, 2]
+        if i == 2 and E > 4:     # fewer numbers than choices
+            for x in (many, one):
+                x.router[0, 1:E - K + 2] = float("nan")
+        many.run()
+        one.run()
+        assert t.equal(one.ids[0], many.ids[1])
+        assert t.equal(one.gates[0], many.gates[1]) or (
+            bool((one.gates[0].isnan() == many.gates[1].isnan()).all())
+            and t.equal(one.gates[0].nan_to_num(7.0), many.gates[1].nan_to_num(7.0)))
+        if i == 0:
+            one.check()
