@@ -128,3 +128,47 @@ def test_fp8_experts_share_the_dispatch_s_quantizer():
     c = Moe(6, 256, 128, 4, 2, "fp8", "bf16", seed=40)
     c.run()
     c.check()
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls that overlap in time on workspaces of their own: each one's bits are
+    those of the call alone."""
+    from tests.test_gpu_clip import tensors
+    from tests.test_gpu_linear import Grad, Linear
+    from tests.test_gpu_moe_layer import Moe
+    o, t = ovl(), fu.torch()
+    src = tensors([70000, 31, 30000])
+
+    class Clip:
+        def __init__(self):
+            self.out = [t.empty_like(v) for v in src]
+            self.plan = o.grad_clip_plan(src, self.out)
+            self.ws, self.norm = fu.workspace(self.plan.workspace_bytes), t.zeros(1, device="cuda")
+            o.grad_clip_upload(self.plan, self.ws)
+
+        def run(self):
+            o.grad_norm_clip_run(self.plan, 0.5, self.norm, self.ws)
+
+    def results(c):
+        return [getattr(c, n) for n in ("out", "z", "da", "db", "dbias", "norm", "gates") if t.is_tensor(getattr(c, n, None))] \
+            + (c.out if isinstance(c, Clip) else [])
+
+    def calls():
+        return [Linear(300, 264, 520), Linear(1, 2048, 4096), Grad(700, 264, 136), Moe(1, 1024, 512, 16, 2),
+                Moe(9, 512, 256, 8, 2, "fp8"), Clip()]
+
+    alone, left, right = calls(), calls(), calls()
+    for c in alone:
+        c.run()
+    t.cuda.synchronize()
+    streams = t.cuda.Stream(), t.cuda.Stream()
+    for _ in range(3):
+        for s, cs in zip(streams, (left, right[::-1])):
+            s.wait_stream(t.cuda.current_stream())
+            with t.cuda.stream(s):
+                for c in cs:
+                    c.run()
+        t.cuda.synchronize()
+        for want, a, b in zip(alone, left, right):
+            for x, y, z in zip(results(want), results(a), results(b)):
+                assert t.equal(x, y) and t.equal(x, z)
