@@ -588,8 +588,8 @@ class GradClipPlan:
     def __init__(self, src, dst=None):
         """src: tensors (bfloat16 or float32); dst: as many (None entries: only in the norm), or None to clip in place."""
         import torch
-        dst = list(src) if dst is None else list(dst)
         src = list(src)
+        dst = list(src) if dst is None else list(dst)
         if len(src) != len(dst):
             raise OvlError(OVL_EINVAL, "grad_clip_plan: as many outputs as inputs")
         buf = _Buffers("grad_clip_plan")

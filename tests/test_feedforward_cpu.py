@@ -241,3 +241,12 @@ def test_moe_layer_refuses_overlaps():
     o = ovl()
     for out in Q[:3]:
         assert moe(o, x=Q[0], w1=Q[1], w2=Q[2], out=out, router=Q[4], topk=Q[5], gates=Q[6], ws=Q[7])[0] == o.OVL_EINVAL
+
+
+def test_grad_clip_plan_takes_a_generator():
+    """Host tensors are refused for where they lie, not for the iterable's kind."""
+    import torch
+    o = ovl()
+    assert len(o.grad_clip_plan(iter([])).tensors[0]) == 0
+    with pytest.raises(o.OvlError, match="current device"):
+        o.grad_clip_plan(torch.zeros(4) for _ in range(2))
