@@ -13,7 +13,7 @@
 // second launch sums them in range order and applies the epilogue.
 //
 // Measured, with what bounds them: forward 8192 x 3584 x 4096 with bias and
-// GELU 229 us (matrix units and power); gradient 8192 x 4096 x 1792 232 us
+// GELU 229-232 us (matrix units and power); gradient 8192 x 4096 x 1792 232-237 us
 // (the same, 1.04 PFLOP/s over both products); 1000 x 2056 x 520 13 us and the
 // gradient of 700 x 2056 x 520 17 us (latency: a launch, 9 and 17 K steps, an
 // epilogue, a second launch in the latter); 1 x 7168 x 8192 24.2 us (HBM, 117

@@ -21,8 +21,8 @@
 //
 // Measured (4096 x 1408, 64 experts, gated): one token, top 2, bf16 33.4 us, of
 // which 12 is the 70 MB stream and the rest the three launches' starts and ends;
-// 64 tokens, top 2, bf16 343 us (HBM: 1.85 GB, up 5.6 and down 5.4 TB/s); 9
-// tokens, top 4, FP8 101 us (HBM: 437 MB, up 4.8 and down 3.9 TB/s).
+// 64 tokens, top 2, bf16 343-360 us (HBM: 1.85 GB, up 5.6 and down 5.4 TB/s); 9
+// tokens, top 4, FP8 101-107 us (HBM: 437 MB, up 4.8 and down 3.9 TB/s).
 #include <algorithm>
 
 #include "epilogue.h"
