@@ -39,6 +39,7 @@ constexpr int kMoeRouteTokens = 4;   // tokens of a routing group (1 where there
 // Arrival counters: down tiles, then (expert, up tile).
 constexpr int32_t kMoeDownCounters = 1024;
 constexpr int kMoeGroups = 256;  // workgroups of the experts' launches: one a compute unit
+constexpr int kMoePlanes = 3;    // of h: 24 bits, as many as a float32 has
 
 struct MoeArgs {
   const uint16_t* x;
@@ -412,9 +413,12 @@ struct MoeGen {
   __device__ inline bool last_of_item() const { return c_first + N >= c_count; }
 };
 
-// h as bf16 planes whose sum is h to 8 bits a plane.
-__device__ inline void moe_store_h(const MoeArgs& a, int planes, int pair, int64_t col, float (&h)[8]) {
-  for (int p = 0; p < planes; ++p) {
+// h as bf16 planes whose sum is h to 8 bits a plane.  (Two planes, 16 bits, left
+// 0.2% of the bf16 outputs a step off; the third costs the down launch nothing
+// where a unit holds few rows, and where codes have many rows an expert, whose
+// units then hold 8 instead of 16, 64 tokens, top 2 of 16, 97 us instead of 86.)
+__device__ inline void moe_store_h(const MoeArgs& a, int pair, int64_t col, float (&h)[8]) {
+  for (int p = 0; p < kMoePlanes; ++p) {
     store8(h, a.h, ((int64_t)p * a.pairs + pair) * a.inter + col, OVL_BF16);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -426,12 +430,12 @@ __device__ inline void moe_store_h(const MoeArgs& a, int planes, int pair, int64
 
 // One pair's eight columns of the up product: scale, activation, h.
 template <class C>
-__device__ inline void moe_act(const MoeArgs& a, int planes, int pair, int64_t col, float (&g)[8], float (&u)[8]) {
+__device__ inline void moe_act(const MoeArgs& a, int pair, int64_t col, float (&g)[8], float (&u)[8]) {
   act8(g, a.act);
   if (C::PAIR)
 #pragma unroll
     for (int c = 0; c < 8; ++c) g[c] *= u[c];
-  moe_store_h(a, planes, pair, col, g);
+  moe_store_h(a, pair, col, g);
 }
 
 // v times the scales of columns col .. of half `half` of unit u.
@@ -449,7 +453,7 @@ __device__ inline void moe_scale(float (&v)[8], const MoeScales* sc, int32_t u, 
 }
 
 template <class C>
-__global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a, int planes) {
+__global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
   extern __shared__ __align__(16) uint8_t moe_lds[];
   __shared__ MoeLds<C::ROWS> s;
   __shared__ __align__(16) uint8_t sc[C::FP8 ? sizeof(MoeScales) : 16];
@@ -491,7 +495,7 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a, int planes)
         store8_agent(g, p);
         if (C::PAIR) store8_agent(v, p + a.inter);
       } else {
-        moe_act<C>(a, planes, pair, col, g, v);
+        moe_act<C>(a, pair, col, g, v);
       }
     }
     if (gen.ranges == 1 || !gen.last_of_item()) return;
@@ -503,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a, int planes)
       if (lds_word(s.ids + pair) != e || col >= a.inter) continue;
       float v[C::PAIR ? 2 : 1][8];
       row_ranges8(v, a.up + pair * a.n1 + col, gen.ranges, a.pairs * a.n1, a.inter);
-      moe_act<C>(a, planes, pair, col, v[0], v[C::PAIR ? 1 : 0]);
+      moe_act<C>(a, pair, col, v[0], v[C::PAIR ? 1 : 0]);
     }
     wave_drain();
   });
@@ -604,7 +608,7 @@ __global__ __launch_bounds__(kThreads) void moe_sum_kernel(MoeArgs a) {
 // ---------------------------------------------------------------- host
 
 struct MoeShape {
-  int32_t pairs, planes, chunks;
+  int32_t pairs, chunks;
   bool few, many;  // pairs an expert: at most 1.5, more than 6
   int32_t up_tiles, up_max, up_steps;
   int32_t down_tiles, down_max, down_steps;
@@ -626,7 +630,6 @@ MoeShape moe_shape(const moe_layer_desc& d) {
   const bool fp8 = d.w_type == OVL_FP8;
   const int ks = fp8 ? 128 : 32;
   s.pairs = (int32_t)(d.tokens * d.topk);
-  s.planes = d.out_type == OVL_F32 ? 3 : 2;
   s.chunks = (int32_t)ceil_div(d.hidden, kMoeRouteRows);
   s.few = 2 * s.pairs <= 3 * d.experts;
   s.many = s.pairs > 6 * d.experts;
@@ -644,7 +647,7 @@ MoeShape moe_shape(const moe_layer_desc& d) {
     off += aligned_up((size_t)bytes, 256);
     return at;
   };
-  s.h_off = take(s.planes * pairs * d.inter * 2);
+  s.h_off = take(kMoePlanes * pairs * d.inter * 2);
   s.up_off = take(s.up_max > 1 ? s.up_max * pairs * n1 * 4 : 0);
   s.down_off = take(s.down_max * pairs * d.hidden * 4);
   s.logits_off = take((int64_t)s.chunks * d.tokens * d.experts * 8);
@@ -669,10 +672,10 @@ ovl_status moe_check(const moe_layer_desc& d) {
 }
 
 template <class C>
-ovl_status moe_up(const MoeArgs& a, int planes, hipStream_t stream) {
+ovl_status moe_up(const MoeArgs& a, hipStream_t stream) {
   ovl_status st = allow_lds(reinterpret_cast<const void*>(&moe_up_kernel<C>), C::LDS);
   if (st) return st;
-  hipLaunchKernelGGL((moe_up_kernel<C>), dim3(kMoeGroups), dim3(kThreads), C::LDS, stream, a, planes);
+  hipLaunchKernelGGL((moe_up_kernel<C>), dim3(kMoeGroups), dim3(kThreads), C::LDS, stream, a);
   OVL_HIP_TRY(hipGetLastError());
   return OVL_OK;
 }
@@ -710,29 +713,23 @@ ovl_status moe_route(const MoeArgs& a, hipStream_t stream) {
 // tokens; their rows take a slot from the down launch's ring (64 tokens, top 2
 // of 64: 133 us with two blocks, 113 with one).
 template <int NB>
-ovl_status moe_bf16(const MoeArgs& a, bool gated, int planes, hipStream_t stream) {
-  const ovl_status st = gated ? moe_up<RowCfg<false, true, 1, NB, 1, kMoeRing>>(a, planes, stream)
-                              : moe_up<RowCfg<false, false, 1, NB, 1, kMoeRing>>(a, planes, stream);
-  if (st) return st;
-  return planes == 2 ? moe_down<RowCfg<false, false, 2, NB, 2, kMoeRing>>(a, stream)
-                     : moe_down<RowCfg<false, false, 3, NB, 2, kMoeRing>>(a, stream);
+ovl_status moe_bf16(const MoeArgs& a, bool gated, hipStream_t stream) {
+  const ovl_status st = gated ? moe_up<RowCfg<false, true, 1, NB, 1, kMoeRing>>(a, stream)
+                              : moe_up<RowCfg<false, false, 1, NB, 1, kMoeRing>>(a, stream);
+  return st ? st : moe_down<RowCfg<false, false, kMoePlanes, NB, 2, kMoeRing>>(a, stream);
 }
 
 // Codes: a step's rows take as much LDS as its weights, so that few rows leave
 // a deeper ring: 4 a unit where an expert has few tokens, else what fits.
-ovl_status moe_fp8(const MoeArgs& a, bool gated, int planes, bool few, hipStream_t stream) {
+ovl_status moe_fp8(const MoeArgs& a, bool gated, bool few, hipStream_t stream) {
   if (few) {
-    const ovl_status st = gated ? moe_up<RowCfg<true, true, 1, 1, 1, kMoeRing, 4>>(a, planes, stream)
-                                : moe_up<RowCfg<true, false, 1, 1, 2, kMoeRing, 4>>(a, planes, stream);
-    if (st) return st;
-    return planes == 2 ? moe_down<RowCfg<true, false, 2, 1, 2, kMoeRing, 4>>(a, stream)
-                       : moe_down<RowCfg<true, false, 3, 1, 2, kMoeRing, 4>>(a, stream);
+    const ovl_status st = gated ? moe_up<RowCfg<true, true, 1, 1, 1, kMoeRing, 4>>(a, stream)
+                                : moe_up<RowCfg<true, false, 1, 1, 2, kMoeRing, 4>>(a, stream);
+    return st ? st : moe_down<RowCfg<true, false, kMoePlanes, 1, 2, kMoeRing, 4>>(a, stream);
   }
-  const ovl_status st = gated ? moe_up<RowCfg<true, true, 1, 2, 1, kMoeRing>>(a, planes, stream)
-                              : moe_up<RowCfg<true, false, 1, 2, 2, kMoeRing>>(a, planes, stream);
-  if (st) return st;
-  return planes == 2 ? moe_down<RowCfg<true, false, 2, 1, 2, kMoeRing>>(a, stream)
-                     : moe_down<RowCfg<true, false, 3, 1, 2, kMoeRing, 8>>(a, stream);
+  const ovl_status st = gated ? moe_up<RowCfg<true, true, 1, 2, 1, kMoeRing>>(a, stream)
+                              : moe_up<RowCfg<true, false, 1, 2, 2, kMoeRing>>(a, stream);
+  return st ? st : moe_down<RowCfg<true, false, kMoePlanes, 1, 2, kMoeRing, 8>>(a, stream);
 }
 
 }  // namespace
@@ -806,6 +803,6 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
                           : (d->experts <= 128 ? moe_route<128>(a, stream) : moe_route<256>(a, stream));
     if (st) return st;
   }
-  if (fp8) return moe_fp8(a, d->gated, s.planes, s.few, stream);
-  return s.many ? moe_bf16<2>(a, d->gated, s.planes, stream) : moe_bf16<1>(a, d->gated, s.planes, stream);
+  if (fp8) return moe_fp8(a, d->gated, s.few, stream);
+  return s.many ? moe_bf16<2>(a, d->gated, stream) : moe_bf16<1>(a, d->gated, stream);
 }

@@ -20,7 +20,7 @@
 // instruction: with steps of 64 codes, half a line each, the experts' launch
 // streamed at 4.1 TB/s, with the next step's half just behind it.
 // PL: x comes as that many bf16 planes whose sum is the value, each
-// multiplied on its own (a float32 h as 2 or 3 planes: 16 or 24 bits).
+// multiplied on its own (a float32 h as 3 planes: 24 bits).
 // LDS rows are XOR-permuted in 16-byte chunks, as in gemm_core.h.
 #pragma once
 
