@@ -68,14 +68,20 @@ struct MoeArgs {
 
 // ---------------------------------------------------------------- routing
 
-// exp(x) of a float64 x, within two float32 steps: the hardware's exp2 of the
-// fraction, scaled (the device library's float64 exp is exact to the last
-// bits, and its code is long to fetch).
-__device__ inline float moe_exp(double x) {
-  const double y = x * 1.4426950408889634074;
-  if (y < -160.0) return 0.f;
-  const double n = rint(y);
-  return ldexpf(__builtin_amdgcn_exp2f((float)(y - n)), (int)n);
+// exp(x) of a float64 x <= 0 to 1e-12 of itself, so that a gate is rounded
+// once: x = n ln 2 + r with |r| <= ln 2 / 2, and the exponential series of r up
+// to r^10 / 10!, whose next term is below 3e-13.  (The device library's float64
+// exp is exact to the last bits, and its code is long to fetch.)
+__device__ inline double moe_exp(double x) {
+  if (x < -740.0) return 0.0;
+  const double n = rint(x * 1.4426950408889634074);
+  const double r = fma(-n, 0.69314718055994530942, x);
+  double p = 1.0 / 3628800;
+  constexpr double kTerms[] = {1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120,
+                               1.0 / 24,     1.0 / 6,     0.5,        1.0,       1.0};
+#pragma unroll
+  for (int i = 0; i < 10; ++i) p = fma(p, r, kTerms[i]);
+  return ldexp(p, (int)n);
 }
 
 __device__ inline double moe_wave_max(double v) {
@@ -101,7 +107,7 @@ __device__ inline MoeChoice moe_pick(const MoeArgs& a, const double* logits) {
     v[i] = have[i] ? logits[lane + 64 * i] : 0.0;
   }
   double first = 0;  // the first choice's logit
-  float chosen = 0.f, mine = 0.f;
+  double chosen = 0, mine = 0;
   int my_id = 0;
   for (int j = 0; j < a.topk_n; ++j) {
     double m = -HUGE_VAL;
@@ -127,7 +133,7 @@ __device__ inline MoeChoice moe_pick(const MoeArgs& a, const double* logits) {
     for (int i = 0; i < 4; ++i)
       if (lane + 64 * i == id) have[i] = false;
     if (j == 0) first = m;
-    const float p = moe_exp(m - first);
+    const double p = moe_exp(m - first);
     chosen += p;
     if (lane == j) {
       mine = p;
@@ -135,14 +141,14 @@ __device__ inline MoeChoice moe_pick(const MoeArgs& a, const double* logits) {
     }
   }
   if (!a.norm_topk) {
-    chosen = 0.f;
+    chosen = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (lane + 64 * i < a.experts) chosen += moe_exp(v[i] - first);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) chosen += __shfl_xor(chosen, d, 64);
   }
-  return {my_id, mine / chosen};
+  return {my_id, (float)(mine / chosen)};
 }
 
 // Workgroup (range of hidden, TT tokens): EP lanes across the experts, 256 /

@@ -4,6 +4,7 @@ inputs of which one bit, one tail or one infinity decides the output."""
 import numpy as np
 import pytest
 
+import oracle
 from tests import ffn_util as fu
 from tests.gpu_util import say
 
@@ -50,3 +51,20 @@ def test_h_keeps_the_bits_of_float32(T, E, w, out):
     want = t.zeros(T, 64, dtype=t.float64, device="cuda")
     want[:, 5] = last
     assert t.equal(c.out[:T].double(), want)
+
+
+@pytest.mark.parametrize("T", [1, 5, 128])
+@pytest.mark.parametrize("E,K", [(8, 2), (64, 8), (200, 4)])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("sigma", [1.0, 40.0])
+def test_gates_are_rounded_once(T, E, K, norm, sigma):
+    """A gate is the float64 softmax rounded to float32: half a step, and 2^-30
+    of it for the float64 sums (a logit of size 300 is off by 2^-44 of it)."""
+    from tests.test_gpu_moe_layer import Moe
+    c = Moe(T, 256, 16, E, K, norm=norm, seed=T)
+    c.router = fu.normal(7, 256, E, sigma=sigma / 16)
+    c.run()
+    ids, gates = oracle.route(fu.f64(c.x) @ fu.f64(c.router), K, norm)
+    assert np.array_equal(c.ids.cpu().numpy(), ids)
+    # below the normal range a float32 step is 2^-149
+    fu.within(c.gates, gates, (fu.U + 2.0 ** -30) * gates + 2.0 ** -149, "gates")
