@@ -419,19 +419,29 @@ struct MoeGen {
   __device__ inline bool last_of_item() const { return c_first + N >= c_count; }
 };
 
-// h as bf16 planes whose sum is h to 8 bits a plane.  (Two planes, 16 bits, left
-// 0.2% of the bf16 outputs a step off; the third costs the down launch nothing
-// where a unit holds few rows, and where codes have many rows an expert, whose
-// units then hold 8 instead of 16, 64 tokens, top 2 of 16, 97 us instead of 86.)
-__device__ inline void moe_store_h(const MoeArgs& a, int pair, int64_t col, float (&h)[8]) {
-  for (int p = 0; p < kMoePlanes; ++p) {
-    store8(h, a.h, ((int64_t)p * a.pairs + pair) * a.inter + col, OVL_BF16);
+// h as three bf16 planes that add up to it: the upper 16 bits of what is left,
+// cut off and not rounded, so that every plane has h's sign and none is larger
+// than h.  Where nothing is left, the planes before it are halved (a quarter and
+// a quarter where there is one): none is zero unless h is, and an infinite
+// weight times each of them is the infinity that it is times h.  (Two planes, 16
+// bits, left 0.2% of the bf16 outputs a step off; the third costs the down
+// launch nothing where a unit holds few rows, and where codes have many rows an
+// expert, whose units then hold 8 instead of 16, 64 tokens, top 2 of 16, 97 us
+// instead of 86.)
+__device__ inline float moe_top(float x) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xFFFF0000u); }
+
+__device__ inline void moe_store_h(const MoeArgs& a, int pair, int64_t col, const float (&h)[8]) {
+  float p[kMoePlanes][8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float b = bf16_lo_f(bf16_bits(h[c]));
-      h[c] = isfinite(b) ? h[c] - b : 0.f;  // an infinity or NaN stands in the first plane alone
-    }
+  for (int c = 0; c < 8; ++c) {
+    const float x = h[c], p0 = moe_top(x), r1 = x - p0, p1 = moe_top(r1), r2 = r1 - p1;
+    const bool one = !(r1 != 0.f) || !isfinite(x), two = r2 == 0.f;
+    p[0][c] = one ? 0.5f * x : p0;
+    p[1][c] = one ? 0.25f * x : (two ? 0.5f * p1 : p1);
+    p[2][c] = one ? 0.25f * x : (two ? 0.5f * p1 : r2);
   }
+#pragma unroll
+  for (int q = 0; q < kMoePlanes; ++q) store8(p[q], a.h, ((int64_t)q * a.pairs + pair) * a.inter + col, OVL_BF16);
 }
 
 // One pair's eight columns of the up product: scale, activation, h.

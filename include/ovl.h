@@ -599,8 +599,7 @@ ovl_status gemm_epilogue_grad_run(const gemm_epilogue_grad_desc* desc, const voi
  * With router NULL the caller's topk_idx and gates are read instead; ids
  * outside [0, experts) (an expert of another rank) contribute nothing, and an
  * id may stand more than once.  Sums and h are float32 (h enters the matrix
- * units as three bf16 terms, 24 bits, so an infinite weight in w2 makes its
- * column NaN); out is rounded once.  The same call gives the same bits every
+ * units as three bf16 terms of its sign, 24 bits); out is rounded once.  The same call gives the same bits every
  * time; how k is cut into ranges, and with it the last bits of a token's
  * row, goes by how many distinct experts the call's tokens chose.
  * ---------------------------------------------------------------------- */

@@ -68,3 +68,60 @@ def test_gates_are_rounded_once(T, E, K, norm, sigma):
     assert np.array_equal(c.ids.cpu().numpy(), ids)
     # below the normal range a float32 step is 2^-149
     fu.within(c.gates, gates, (fu.U + 2.0 ** -30) * gates + 2.0 ** -149, "gates")
+
+
+@pytest.mark.parametrize("w", ["bf16"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 9])
+def test_an_infinite_second_weight_gives_what_the_product_gives(T, out, w):
+    """h times an infinite weight is the infinity of h's sign, whether h has one
+    significant bit or 24; zero times it is NaN, and so are two opposite ones."""
+    from tests.test_gpu_moe_layer import Moe
+    t = fu.torch()
+    inf = float("inf")
+    c = Moe(T, 64, 32, 4, 1, w, out, "none", False, route=False, seed=1)
+    c.x.zero_()
+    c.w1.zero_()
+    c.w2.zero_()
+    c.gates.fill_(0.5)
+    # h of columns 0..5: 1, -3 * 2^-5, 1 + 2^-9, -(1 + 2^-9 + 2^-20), 0, the largest bf16
+    c.x[:, :3] = t.tensor([1.0, 2.0 ** -9, 2.0 ** -20], device="cuda")
+    big = float(t.finfo(t.bfloat16).max)
+    for e in range(4):
+        c.w1[e, :3, :6] = t.tensor([[1.0, -3 / 32, 1.0, -1.0, 0.0, big], [0, 0, 1.0, -1.0, 0, 0], [0, 0, 0, -1.0, 0, 0]])
+        for i in range(6):
+            c.w2[e, i, i] = inf
+            c.w2[e, i, 8 + i] = -inf
+        c.w2[e, 0, 16], c.w2[e, 3, 16] = inf, inf   # opposite infinities
+        c.w2[e, 0, 17], c.w2[e, 1, 17] = inf, 1.0   # beside a finite term
+        c.w2[e, 2, 18] = 2.0                        # no infinity
+    c.run()
+    got = c.out[:T].float().cpu()
+    nan = float("nan")
+    want = t.zeros(64)
+    want[:6] = t.tensor([inf, -inf, inf, -inf, nan, inf])
+    want[8:14] = t.tensor([-inf, inf, -inf, inf, nan, -inf])
+    want[16], want[17], want[18] = nan, inf, 1.0 + 2.0 ** -9
+    want = want.to(fu.ttype(out)).float()
+    # zero weights of finite h add nothing: every other column is exactly zero
+    for i in range(T):
+        assert t.equal(got[i].isnan(), want.isnan())
+        assert t.equal(got[i].nan_to_num(7.0, inf, -inf), want.nan_to_num(7.0, inf, -inf))
+
+
+def test_an_infinite_h_stays_one():
+    """An infinite activation times finite weights: infinities, NaN at zero weights."""
+    from tests.test_gpu_moe_layer import Moe
+    t = fu.torch()
+    c = Moe(2, 64, 32, 2, 1, "bf16", "f32", "none", False, route=False, seed=1)
+    c.x.zero_()
+    c.x[:, 0] = 1.0
+    c.w1.zero_()
+    c.w1[:, 0, 4] = float("inf")
+    c.w2.fill_(1.0)
+    c.w2[:, 4, 1] = -2.0
+    c.w2[:, 4, 2] = 0.0
+    c.gates.fill_(1.0)
+    c.run()
+    assert bool((c.out[:2, 0] == float("inf")).all()) and bool((c.out[:2, 1] == -float("inf")).all())
+    assert bool(c.out[:2, 2].isnan().all()) and bool((c.out[:2, 3:] == float("inf")).all())
