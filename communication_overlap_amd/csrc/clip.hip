@@ -28,13 +28,16 @@
 // entries are addresses: every entry carries a tag made of its contents, its
 // number and its plan's, and a wavefront that meets one whose tag is wrong
 // (never uploaded, another plan's, written over since) touches nothing that
-// it names.  The run then reports EINVAL, gives a NaN norm and scales nothing.
+// it names.  Its verdict travels apart from the sums (clip_sum.h), so that an
+// infinity or a NaN among the gradients does not hide it.  The run then reports
+// EINVAL, gives a NaN norm and scales nothing.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <new>
 #include <vector>
 
+#include "clip_sum.h"
 #include "device.h"
 #include "host.h"
 
@@ -183,8 +186,8 @@ struct GcTensor {
 
 constexpr int kGcU = 4;  // 16-byte loads in flight per lane
 
-// Sum of squares over slots [v0, v1), this lane's share; minus infinity where
-// the table is not this plan's.  (Sound entries follow each other without a
+// Sum of squares over slots [v0, v1), this lane's share; kClipForeign, in every
+// lane, where the table is not this plan's.  (Sound entries follow each other without a
 // gap up to the last slot, so a walk from the one that holds v0 stays in the
 // table.  Every entry holds slots, so that the launch looks at all of them.)
 __device__ inline double gc_sum_range(const GcArgs& a, int64_t v0, int64_t v1) {
@@ -197,7 +200,7 @@ __device__ inline double gc_sum_range(const GcArgs& a, int64_t v0, int64_t v1) {
     const uint64_t tag = gc_tag(entry, t, a.plan);
     if (entry.tag != tag || v0 < entry.first || v0 >= entry.end) {
       if (lane == 0) report_error(a.err, OVL_EINVAL, kSiteClip, t, (int64_t)entry.tag, (int64_t)tag);
-      return -HUGE_VAL;
+      return kClipForeign;
     }
     const GcTensor g(entry);
     const int64_t b = v0 - g.first, e = min(v1 - g.first, g.slots);
@@ -294,20 +297,23 @@ __device__ inline double gc_wave_sum(double s) {
   return s;
 }
 
-// Sum over the workgroup's threads, the same bits in every thread.
+// Total over the workgroup's threads, the same bits in every thread; s as
+// ClipTotal::add takes it.
 template <int NT>
-__device__ inline double gc_group_sum(double s, double* lds) {
+__device__ inline ClipTotal gc_group_sum(double s, double* lds) {
+  const bool foreign = __any(s < 0);
   s = gc_wave_sum(s);
-  if (lane_id() == 0) lds[threadIdx.x >> 6] = s;
+  if (lane_id() == 0) lds[threadIdx.x >> 6] = foreign ? kClipForeign : s;
   __syncthreads();
-  s = 0;
+  ClipTotal t;
 #pragma unroll
-  for (int w = 0; w < NT / 64; ++w) s += lds[w];
-  return s;
+  for (int w = 0; w < NT / 64; ++w) t.add(lds[w]);
+  return t;
 }
 
-__device__ inline float gc_coef(const GcArgs& a, double sum, bool first) {
-  const double norm = sqrt(sum);  // NaN for a sum below 0
+// norm by the first thread; NaN where the table is foreign.
+__device__ inline float gc_coef(const GcArgs& a, const ClipTotal& t, bool first) {
+  const double norm = t.foreign ? __builtin_nan("") : sqrt(t.sum);
   if (first) *a.norm = (float)norm;
   const double c = (double)a.max_norm / (norm + 1e-6);
   return c >= 1.0 || isinf(a.max_norm) ? 1.f : (float)c;  // a NaN norm gives a NaN coefficient
@@ -317,23 +323,23 @@ __global__ __launch_bounds__(kThreads) void gc_norm_kernel(GcArgs a) {
   __shared__ double lds[kThreads / 64];
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 64) + uniform(threadIdx.x >> 6);
   const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
-  const double s = gc_group_sum<kThreads>(gc_sum_range(a, v0, v1), lds);
-  if (threadIdx.x == 0) a.sums[blockIdx.x] = s;
+  const ClipTotal t = gc_group_sum<kThreads>(gc_sum_range(a, v0, v1), lds);
+  if (threadIdx.x == 0) a.sums[blockIdx.x] = t.word();
 }
 
 __global__ __launch_bounds__(kThreads) void gc_scale_kernel(GcArgs a) {
   __shared__ double lds[kThreads / 64];
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 64) + uniform(threadIdx.x >> 6);
   const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
-  double s = 0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) s += a.sums[i];
+  ClipTotal mine;
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) mine.add(a.sums[i]);
   // (The search's loads are on their way with the sums'.)
-  int64_t t = 0;
-  GcEntry entry = gc_find(a.table, a.tensors, max(v1 - 1, (int64_t)0), t);
-  s = gc_group_sum<kThreads>(s, lds);
-  const float coef = gc_coef(a, s, blockIdx.x == 0 && threadIdx.x == 0);
-  if (s < 0) return;  // not this plan's table
-  gc_scale_range(a, v0, v1, entry, t, coef);
+  int64_t at = 0;
+  GcEntry entry = gc_find(a.table, a.tensors, max(v1 - 1, (int64_t)0), at);
+  const ClipTotal t = gc_group_sum<kThreads>(mine.word(), lds);
+  const float coef = gc_coef(a, t, blockIdx.x == 0 && threadIdx.x == 0);
+  if (t.foreign) return;
+  gc_scale_range(a, v0, v1, entry, at, coef);
 }
 
 constexpr int kGcOneThreads = 1024;
@@ -342,12 +348,13 @@ __global__ __launch_bounds__(kGcOneThreads) void gc_one_kernel(GcArgs a) {
   __shared__ double lds[kGcOneThreads / 64];
   const int64_t w = uniform(threadIdx.x >> 6);
   const int64_t v0 = min(w * a.per_wave, a.slots), v1 = min(v0 + a.per_wave, a.slots);
-  const double s = gc_group_sum<kGcOneThreads>(gc_sum_range(a, v0, v1), lds);
-  const float coef = gc_coef(a, s, threadIdx.x == 0);
-  if (s < 0 || v0 >= v1) return;
-  int64_t t;
-  const GcEntry entry = gc_find(a.table, a.tensors, v1 - 1, t);
-  gc_scale_range(a, v0, v1, entry, t, coef);
+  const ClipTotal t = gc_group_sum<kGcOneThreads>(gc_sum_range(a, v0, v1), lds);
+  const float coef = gc_coef(a, t, threadIdx.x == 0);
+  if (t.foreign) return;
+  if (v0 >= v1) return;
+  int64_t at;
+  const GcEntry entry = gc_find(a.table, a.tensors, v1 - 1, at);
+  gc_scale_range(a, v0, v1, entry, at, coef);
 }
 
 }  // namespace
