@@ -1,6 +1,8 @@
 """Values of the feed-forward calls that bounds over random data do not see:
 inputs of which one bit, one tail or one infinity decides the output."""
 
+import math
+
 import numpy as np
 import pytest
 
@@ -125,3 +127,72 @@ def test_an_infinite_h_stays_one():
     c.run()
     assert bool((c.out[:2, 0] == float("inf")).all()) and bool((c.out[:2, 1] == -float("inf")).all())
     assert bool(c.out[:2, 2].isnan().all()) and bool((c.out[:2, 3:] == float("inf")).all())
+
+
+# ------------------------------------------------------------------ activations' tails
+
+def activation(act, z):
+    """act at the float32 values z: a product of zeros with z as its bias."""
+    o, t = ovl(), fu.torch()
+    n = -(-len(z) // 8) * 8
+    bias = t.zeros(n, device="cuda")
+    bias[:len(z)] = t.from_numpy(z).cuda()
+    a, b = (t.zeros(*s, dtype=t.bfloat16, device="cuda") for s in ((3, 8), (8, n)))
+    out = t.empty(3, n, device="cuda")
+    d = o.gemm_epilogue_desc(3, n, 8, act, "f32")
+    say(f"  gemm_epilogue_run of {n} pre-activations, {act}")
+    o.gemm_epilogue_run(d, a, b, bias, None, out, None, fu.workspace(o.gemm_epilogue_workspace_bytes(d)))
+    assert t.equal(out[0], out[2])
+    return fu.f64(out[0, :len(z)])
+
+
+def derivative(act, z):
+    """act' at the bf16 values z: the factor of a product of ones."""
+    o, t = ovl(), fu.torch()
+    k = -(-len(z) // 8) * 8
+    z_in = t.zeros(2, k, dtype=t.bfloat16, device="cuda")
+    z_in[:, :len(z)] = t.from_numpy(z).cuda()
+    dz, b = (t.zeros(r, 8, dtype=t.bfloat16, device="cuda") for r in (2, k))
+    dz[:, 0], b[:, 0] = 1.0, 1.0
+    da = t.empty(2, k, device="cuda")
+    d = o.gemm_epilogue_grad_desc(2, 8, k, "none", act, "bf16", "f32", "f32")
+    say(f"  gemm_epilogue_grad_run of {k} pre-activations, {act}")
+    o.gemm_epilogue_grad_run(d, dz, None, b, z_in, da, None, None, None, None,
+                             fu.workspace(o.gemm_epilogue_grad_workspace_bytes(d)))
+    assert t.equal(da[0], da[1])
+    return fu.f64(da[0, :len(z)])
+
+
+def bf16_points(lo, hi):
+    """Every bf16 value of [lo, hi] from 2^-20 up in size."""
+    v = (np.arange(1 << 16, dtype=np.uint32) << 16).view(np.float32)
+    return np.sort(v[np.isfinite(v) & (v >= lo) & (v <= hi) & (np.abs(v) >= 2.0 ** -20)])
+
+
+def closest(got, want, bound, z):
+    bad = ~(np.abs(got - want) <= bound)
+    i = int(np.argmax(bad))
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} off; at z = {z[i]}: {got[i]} against {want[i]}, bound {bound[i]}"
+
+
+def test_gelu_keeps_its_tail():
+    """0.5 z erfc(-z / sqrt 2), relative to itself down to 1e-35.  By way of the
+    error function's argument, off by 2 U of itself (U = 2^-24), erfc(x) moves
+    by 2 x^2 + 1 = z^2 + 1 times as much of itself, and by way of exp(-z^2 / 2)
+    by 1.5 z^2 U, three roundings of the exponent; 34 U are left for the
+    polynomial or erfc's own steps, the exponential and the products."""
+    z = np.linspace(-12.4, 6, 6001).astype(np.float32)
+    want = np.array([0.5 * v * math.erfc(-v / math.sqrt(2.0)) for v in z.astype(np.float64)])
+    closest(activation("gelu", z), want, (2 * (z.astype(np.float64) ** 2 + 1) + 34) * fu.U * np.abs(want), z)
+
+
+def test_gelu_derivative_keeps_its_tail():
+    """cdf + z pdf: the cdf as above; in the pdf the exponent z^2 / 2 is off by 3 U
+    of itself (a constant and two products), the exponential by 2 U more and its
+    two factors by 3 U; one sum."""
+    z = bf16_points(-12.4, 6.0)
+    v = z.astype(np.float64)
+    cdf = np.array([0.5 * math.erfc(-x / math.sqrt(2.0)) for x in v])
+    pdf = np.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    bound = ((2 * (v * v + 1) + 34) * cdf + (1.5 * v * v + 6) * np.abs(v) * pdf) * fu.U
+    closest(derivative("gelu", z), cdf + v * pdf, bound * (1 + 2.0 ** -10) + fu.U * np.abs(cdf + v * pdf), z)
