@@ -13,14 +13,31 @@ __device__ inline float bf16_hi_f(uint32_t w) { return __builtin_bit_cast(float,
 __device__ inline uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 __device__ inline uint32_t bf16_pair(float a, float b) { return bf16_bits(a) | bf16_bits(b) << 16; }
 
-// 1 / (1 + exp(-x)): the hardware's exp2 and reciprocal, both within an ulp
-// or two; exp overflows to infinity, whose reciprocal is the right zero.
-__device__ inline float sigmoid_f(float x) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
-}
+// sigma(x) = 1 / (1 + exp(-x)) and sigma(-x), each to a few float32 steps of
+// itself (2 |x| half steps come from the exponent's rounding): with e = exp(-|x|)
+// = h^2 the greater is r = 1 / (1 + e), the lesser e r.  y times the lesser is
+// taken as (y h) (h r), since e leaves float32's range before y e does.
+struct Sigmoid {
+  float h, r;
+  bool up;
+  __device__ inline explicit Sigmoid(float x) : up(x > 0.f) {
+    h = __builtin_amdgcn_exp2f(fabsf(x) * (-0.5f * 1.44269504088896341f));
+    r = __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.f));
+  }
+  __device__ inline float times(float y) const {
+    const float g = up ? 1.f : h;
+    return (y * g) * (g * r);
+  }
+  __device__ inline float complement() const {
+    const float g = up ? h : 1.f;
+    return g * (g * r);
+  }
+};
 
-constexpr float kGeluR = 0.797884560802865356f;  // sqrt(2 / pi)
-constexpr float kGeluC = 0.044715f;
+// The tanh form of GELU, 0.5 z (1 + tanh u), u = sqrt(2 / pi) (z + 0.044715 z^3),
+// is z sigma(2 u): no cancellation where tanh is near -1.  2 u from z and z^2:
+constexpr float kGelu1 = 1.59576912160573071f, kGelu3 = 0.044715f * kGelu1;
+__device__ inline float gelu_arg(float z, float z2) { return z * __builtin_fmaf(kGelu3, z2, kGelu1); }
 
 // The normal distribution's tail beyond |z|, exp(-z^2 / 2) r, with r a
 // polynomial in t = 1 / (1 + 0.3 |z|): the scaled complementary error function
@@ -42,8 +59,6 @@ struct NormalTail {
   }
 };
 
-// The tanh form of GELU, 0.5 z (1 + tanh u), is z sigmoid(2 u): no
-// cancellation where tanh is near -1.
 __device__ inline float act_f(float z, int kind) {
   switch (kind) {
     case OVL_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
@@ -51,32 +66,34 @@ __device__ inline float act_f(float z, int kind) {
       const NormalTail n(z);
       return z * (z > 0.f ? 1.f - n.e * n.r : n.e * n.r);
     }
-    case OVL_ACT_GELU_TANH: return z * sigmoid_f(2.f * kGeluR * (z + kGeluC * z * z * z));
-    case OVL_ACT_SILU: return z * sigmoid_f(z);
+    case OVL_ACT_GELU_TANH: return Sigmoid(gelu_arg(z, z * z)).times(z);
+    case OVL_ACT_SILU: return Sigmoid(z).times(z);
     default: return z;
   }
 }
 
-// d act / dz.  Beyond |z| = 32 every smooth one is 0 or 1 in float32; taking
-// that keeps infinity times zero out of the products below.
+// d act / dz.  A smooth one's factor z is taken at most so far out that the
+// value has reached 1 there or, below, is under float32's least number (SiLU's: z
+// exp(z), -1e-44 at z = -106; the GELUs': exp(-z^2 / 2)), which keeps infinity
+// times zero out of the products.  NaN stays, by way of the exponential.
 __device__ inline float act_grad_f(float z, int kind) {
-  if (kind == OVL_ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
-  if (kind == OVL_ACT_NONE) return 1.f;
-  const bool far = fabsf(z) > 32.f;
-  const float limit = z > 0.f ? 1.f : 0.f;
   switch (kind) {
+    case OVL_ACT_RELU: return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
     case OVL_ACT_GELU: {  // cdf + z pdf
       const NormalTail n(z);
-      return far ? limit : limit + n.e * (0.398942280401432678f * z + (z > 0.f ? -n.r : n.r));
+      const float v = __builtin_amdgcn_fmed3f(z, -32.f, 32.f);
+      return (z > 0.f ? 1.f : 0.f) + n.e * (0.398942280401432678f * v + (z > 0.f ? -n.r : n.r));
     }
-    case OVL_ACT_GELU_TANH: {
-      const float s = sigmoid_f(2.f * kGeluR * (z + kGeluC * z * z * z));
-      return far ? limit : s + z * s * (1.f - s) * (2.f * kGeluR * (1.f + 3.f * kGeluC * z * z));
+    case OVL_ACT_GELU_TANH: {  // s + z s (1 - s) d(2 u) / dz
+      const float z2 = fminf(z * z, 1024.f), v = __builtin_amdgcn_fmed3f(z, -32.f, 32.f);
+      const Sigmoid s(gelu_arg(z, z2));
+      return s.times(1.f + v * s.complement() * __builtin_fmaf(3.f * kGelu3, z2, kGelu1));
     }
-    default: {
-      const float s = sigmoid_f(z);
-      return far ? limit : s + z * s * (1.f - s);
+    case OVL_ACT_SILU: {  // s + z s (1 - s)
+      const Sigmoid s(z);
+      return s.times(1.f + __builtin_amdgcn_fmed3f(z, -256.f, 256.f) * s.complement());
     }
+    default: return 1.f;
   }
 }
 

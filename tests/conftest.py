@@ -22,3 +22,18 @@ def gemm_tol(k: int, ref_absmax: float) -> float:
 @pytest.fixture(scope="session")
 def tol():
     return gemm_tol
+
+
+# Tests that hold a wrong value, each with the test that holds the right one.
+WRONG_VALUES = {
+    "tests/test_gpu_linear.py::test_grad_derivatives_far_out_are_zero_or_one":
+        "SiLU's derivative at -40 is exp(-40) (1 - 40) = -1.66e-16, a bf16 number, not 0: "
+        "tests/test_gpu_feedforward_bits.py::test_own_derivative_far_out",
+}
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        reason = WRONG_VALUES.get(item.nodeid)
+        if reason:
+            item.add_marker(pytest.mark.xfail(reason=reason, strict=True))

@@ -196,3 +196,74 @@ def test_gelu_derivative_keeps_its_tail():
     pdf = np.exp(-v * v / 2) / math.sqrt(2 * math.pi)
     bound = ((2 * (v * v + 1) + 34) * cdf + (1.5 * v * v + 6) * np.abs(v) * pdf) * fu.U
     closest(derivative("gelu", z), cdf + v * pdf, bound * (1 + 2.0 ** -10) + fu.U * np.abs(cdf + v * pdf), z)
+
+
+def sigmoid(v):
+    """To a few steps of itself on either side: exp(-|v|) is exact to 2^-53 of itself."""
+    e = np.exp(-np.abs(v))
+    return np.where(v > 0, 1.0, e) / (1.0 + e)
+
+
+# sigma(x)'s relative error: the exponent |x| log2(e) / 2 is off by 2 U of itself
+# (constant and product) and taken twice, 2 |x| U; two exponentials 4 U, the
+# reciprocal 2 U, its sum 1 U and three products 3 U.  Results below float32's
+# normal range are rounded to multiples of 2^-149, twice at most.
+def sigma_bound(x):
+    return (2 * np.abs(x) + 12) * fu.U
+
+
+LEAST = 2.0 ** -148
+
+
+def test_silu_and_its_derivative_keep_their_tails():
+    """z sigma(z) down to where it leaves float32, near z = -106, and its
+    derivative s (1 + z (1 - s)), whose inner sum is off by the error of |z| (1 - s)."""
+    z = np.linspace(-120, 20, 14001).astype(np.float32)
+    v = z.astype(np.float64)
+    want = v * sigmoid(v)
+    closest(activation("silu", z), want, sigma_bound(v) * np.abs(want) + LEAST, z)
+    z = bf16_points(-300.0, 300.0)
+    v = z.astype(np.float64)
+    s, t = sigmoid(v), sigmoid(-v)
+    want = s * (1 + v * t)
+    bound = s * (np.abs(1 + v * t) * sigma_bound(v) + np.abs(v) * t * sigma_bound(v) + fu.U) + LEAST
+    got = derivative("silu", z)
+    closest(got, want, bound, z)
+    assert np.abs(got[(z < -80) & (z > -100)]).min() > 0
+
+
+def test_gelu_tanh_and_its_derivative_keep_their_tails():
+    """z sigma(w), w = 2 sqrt(2 / pi) (z + c z^3), off by 6 U of itself (two
+    constants, four products and a sum, of terms of one sign)."""
+    r = 2 * math.sqrt(2 / math.pi)
+    z = np.linspace(-10.5, 6, 6001).astype(np.float32)
+    v = z.astype(np.float64)
+    w = r * (v + 0.044715 * v ** 3)
+    want = v * sigmoid(w)
+    err = sigma_bound(w) + 7 * np.abs(w) * fu.U
+    closest(activation("gelu_tanh", z), want, err * np.abs(want) + LEAST, z)
+    z = bf16_points(-40.0, 40.0)
+    v = z.astype(np.float64)
+    w, d = r * (v + 0.044715 * v ** 3), r * (1 + 3 * 0.044715 * v * v)
+    s, t = sigmoid(w), sigmoid(-w)
+    want = s * (1 + v * t * d)
+    err = sigma_bound(w) + 7 * np.abs(w) * fu.U
+    bound = s * (np.abs(1 + v * t * d) * err + np.abs(v) * t * d * (err + 8 * fu.U) + fu.U) + LEAST
+    closest(derivative("gelu_tanh", z), want, bound, z)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dy", ["bf16", "f32"])
+def test_own_derivative_far_out(act, dy):
+    """dz at pre-activations up to infinity: no 0 * inf on the way, NaN stays
+    NaN, and at -40 SiLU's derivative is exp(-40) (1 - 40), a bf16 number."""
+    t, o = fu.torch(), ovl()
+    z = t.tensor([[3e38, -3e38, math.inf, -math.inf, 40.0, -40.0, math.nan, -300.0]] * 8, device="cuda").bfloat16()
+    dz, ones = t.empty_like(z), t.ones(8, 8, device="cuda", dtype=fu.ttype(dy))
+    d = o.gemm_epilogue_grad_desc(8, 8, 8, act, "none", dy)
+    o.gemm_epilogue_grad_run(d, dz, None, None, None, None, None, None, None, None,
+                             fu.workspace(o.gemm_epilogue_grad_workspace_bytes(d)), ones, z)
+    got = fu.f64(dz[3])
+    assert got[:5].tolist() == [1, 0, 1, 0, 1] and math.isnan(got[6]) and got[7] == 0
+    want = math.exp(-40.0) * (1 - 40.0) if act == "silu" else 0.0
+    assert abs(got[5] - want) <= (fu.HALF["bf16"] + 200 * fu.U) * abs(want)
