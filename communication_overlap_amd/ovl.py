@@ -462,29 +462,48 @@ def _type(t) -> int:
     return TYPES[t] if isinstance(t, str) else t
 
 
+# Element types of buffers beside BF16, F32 and FP8.
+_INT32, _BYTES = 16, 17
+
+
+def _dtypes() -> dict:
+    global _dtype_table
+    if _dtype_table is None:
+        t = _torch()
+        _dtype_table = {BF16: (t.bfloat16, t.int16, t.uint16), F32: (t.float32,), FP8: (t.uint8, t.float8_e4m3fn),
+                        _INT32: (t.int32,), _BYTES: (t.uint8, t.int8, t.bool)}
+    return _dtype_table
+
+
+_dtype_table = None
+
+
 class _Buffers:
     """Marshals the buffers of one call of the feed-forward calls.  A tensor
-    has to lie on the current device, hold elements of the right size and be
-    as large as the call takes it to be (dense, or a two-dimensional view with
-    the descriptor's row stride); raw addresses pass unchecked."""
+    has to lie on the current device, hold elements of the right type (bf16 or
+    its bits as int16 or uint16; E4M3 or its codes as uint8) and be as large as
+    the call takes it to be (dense, or a two-dimensional view with the
+    descriptor's row stride); raw addresses pass unchecked."""
 
-    __slots__ = ("where", "device")
+    __slots__ = ("where", "device", "kinds")
 
     def __init__(self, where: str):
         torch = _torch()
         self.where = where
+        self.kinds = _dtypes()
         self.device = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
 
     def refuse(self, name: str, why: str):
         raise OvlError(OVL_EINVAL, f"{self.where}: {name} {why}")
 
-    def __call__(self, name: str, t, size: int, rows: int, cols: int, ld: int = 0):
+    def __call__(self, name: str, t, kind: int, rows: int, cols: int, ld: int = 0):
         if t is None or isinstance(t, int):
             return t
+        kinds = self.kinds.get(kind)
+        if kinds and t.dtype not in kinds:  # (of a type that the library refuses anything goes)
+            self.refuse(name, f"has elements of type {t.dtype}, not {' or '.join(str(k) for k in kinds)}")
         if t.get_device() != self.device:  # -1: host memory
             self.refuse(name, "is not on the current device")
-        if t.element_size() != size:
-            self.refuse(name, f"has elements of {t.element_size()} bytes, not {size}")
         if t.is_contiguous():
             if rows > 0 and t.numel() < (rows - 1) * (ld or cols) + cols:
                 self.refuse(name, "is too small")
@@ -502,10 +521,7 @@ def _workspace(buf, workspace, nbytes, desc):
     known = getattr(desc, "_workspace", None)
     if known is None or known[0] != key:
         known = desc._workspace = (key, nbytes(byref(desc)))
-    return buf("workspace", workspace, 1, 1, known[1])
-
-
-_SIZE = {BF16: 2, F32: 4, FP8: 1}
+    return buf("workspace", workspace, _BYTES, 1, known[1])
 
 
 def gemm_epilogue_desc(m, n, k, act="none", out_type="bf16", res_type="bf16", lda=0, ldb=0, ldo=0, ldz=0,
@@ -523,9 +539,9 @@ def gemm_epilogue_run(desc: GemmEpilogueDesc, a, b, bias, residual, out, z, work
     buf = _Buffers("gemm_epilogue_run")
     m, n, k = desc.m, desc.n, desc.k
     st = lib().gemm_epilogue_run(
-        byref(desc), buf("a", a, 2, m, k, desc.lda), buf("b", b, 2, k, n, desc.ldb), buf("bias", bias, 4, 1, n),
-        buf("residual", residual, _SIZE.get(desc.res_type, 1), m, n, desc.ldr),
-        buf("out", out, _SIZE.get(desc.out_type, 1), m, n, desc.ldo), buf("z", z, 2, m, n, desc.ldz),
+        byref(desc), buf("a", a, BF16, m, k, desc.lda), buf("b", b, BF16, k, n, desc.ldb), buf("bias", bias, F32, 1, n),
+        buf("residual", residual, desc.res_type, m, n, desc.ldr), buf("out", out, desc.out_type, m, n, desc.ldo),
+        buf("z", z, BF16, m, n, desc.ldz),
         _workspace(buf, workspace, lib().gemm_epilogue_workspace_bytes, desc), _stream(stream))
     return _check(st, "gemm_epilogue_run", raise_on_error)
 
@@ -546,13 +562,12 @@ def gemm_epilogue_grad_run(desc: GemmEpilogueGradDesc, dz, a, b, z_in, da, db, d
     descriptor's act, dz = dy * act'(z) is computed first.  Any of da, db, dbias may be None."""
     buf = _Buffers("gemm_epilogue_grad_run")
     m, n, k = desc.m, desc.n, desc.k
-    db_size = _SIZE.get(desc.db_type, 1)
     st = lib().gemm_epilogue_grad_run(
-        byref(desc), buf("dy", dy, _SIZE.get(desc.dy_type, 1), m, n, desc.lddy), buf("z", z, 2, m, n, desc.ldz),
-        buf("dz", dz, 2, m, n, desc.lddz), buf("a", a, 2, m, k, desc.lda), buf("b", b, 2, k, n, desc.ldb),
-        buf("z_in", z_in, 2, m, k, desc.ldz_in), buf("da", da, _SIZE.get(desc.da_type, 1), m, k, desc.ldda),
-        buf("db", db, db_size, k, n, desc.lddb), buf("db_in", db_in, db_size, k, n, desc.lddb),
-        buf("dbias", dbias, 4, 1, n), buf("dbias_in", dbias_in, 4, 1, n),
+        byref(desc), buf("dy", dy, desc.dy_type, m, n, desc.lddy), buf("z", z, BF16, m, n, desc.ldz),
+        buf("dz", dz, BF16, m, n, desc.lddz), buf("a", a, BF16, m, k, desc.lda), buf("b", b, BF16, k, n, desc.ldb),
+        buf("z_in", z_in, BF16, m, k, desc.ldz_in), buf("da", da, desc.da_type, m, k, desc.ldda),
+        buf("db", db, desc.db_type, k, n, desc.lddb), buf("db_in", db_in, desc.db_type, k, n, desc.lddb),
+        buf("dbias", dbias, F32, 1, n), buf("dbias_in", dbias_in, F32, 1, n),
         _workspace(buf, workspace, lib().gemm_epilogue_grad_workspace_bytes, desc), _stream(stream))
     return _check(st, "gemm_epilogue_grad_run", raise_on_error)
 
@@ -572,12 +587,11 @@ def moe_layer_run(desc: MoeLayerDesc, x, router, topk_idx, gates, w1, w1_scale, 
     """The whole layer for a few tokens; with a router, topk_idx and gates are written, else read."""
     buf = _Buffers("moe_layer_run")
     t, h, i, e, k = desc.tokens, desc.hidden, desc.inter, desc.experts, desc.topk
-    n1, w = (2 * i if desc.gated else i), _SIZE.get(desc.w_type, 1)
+    n1, w = (2 * i if desc.gated else i), desc.w_type
     st = lib().moe_layer_run(
-        byref(desc), buf("x", x, 2, t, h), buf("router", router, 2, h, e), buf("topk_idx", topk_idx, 4, t, k),
-        buf("gates", gates, 4, t, k), buf("w1", w1, w, e * h, n1), buf("w1_scale", w1_scale, 4, e, n1),
-        buf("w2", w2, w, e * i, h), buf("w2_scale", w2_scale, 4, e, h),
-        buf("out", out, _SIZE.get(desc.out_type, 1), t, h),
+        byref(desc), buf("x", x, BF16, t, h), buf("router", router, BF16, h, e), buf("topk_idx", topk_idx, _INT32, t, k),
+        buf("gates", gates, F32, t, k), buf("w1", w1, w, e * h, n1), buf("w1_scale", w1_scale, F32, e, n1),
+        buf("w2", w2, w, e * i, h), buf("w2_scale", w2_scale, F32, e, h), buf("out", out, desc.out_type, t, h),
         _workspace(buf, workspace, lib().moe_layer_workspace_bytes, desc), _stream(stream))
     return _check(st, "moe_layer_run", raise_on_error)
 
@@ -599,10 +613,9 @@ class GradClipPlan:
                 buf.refuse(f"tensor {i}", "is not bfloat16 or float32, or its output is of another type")
             if not s.is_contiguous() or (d is not None and (not d.is_contiguous() or d.numel() != s.numel())):
                 buf.refuse(f"tensor {i}", "is not dense, or its output is of another size")
-            n = s.numel()
-            arr[i] = GradClipTensor(buf(f"tensor {i}", s, s.element_size(), 1, n) or None,
-                                    buf(f"output {i}", d, s.element_size(), 1, n) or None, n,
-                                    F32 if s.dtype == torch.float32 else BF16, 0)
+            n, kind = s.numel(), F32 if s.dtype == torch.float32 else BF16
+            arr[i] = GradClipTensor(buf(f"tensor {i}", s, kind, 1, n) or None, buf(f"output {i}", d, kind, 1, n) or None,
+                                    n, kind, 0)
         self.tensors = (src, dst)
         self.device = buf.device
         h = c_void_p()
@@ -628,7 +641,7 @@ def grad_clip_plan(src, dst=None) -> GradClipPlan:
 def grad_clip_upload(plan: GradClipPlan, workspace, stream=None, raise_on_error: bool = True) -> int:
     buf = _Buffers("grad_clip_upload")
     plan._here(buf)
-    ws = buf("workspace", workspace, 1, 1, plan.workspace_bytes)
+    ws = buf("workspace", workspace, _BYTES, 1, plan.workspace_bytes)
     return _check(lib().grad_clip_upload(plan.handle, ws, _stream(stream)), "grad_clip_upload", raise_on_error)
 
 
@@ -637,8 +650,8 @@ def grad_norm_clip_run(plan: GradClipPlan, max_norm: float, norm, workspace, str
     """norm (float32 [1]) = the global norm; every dst = src * min(1, max_norm / (norm + 1e-6))."""
     buf = _Buffers("grad_norm_clip_run")
     plan._here(buf)
-    st = lib().grad_norm_clip_run(plan.handle, max_norm, buf("norm", norm, 4, 1, 1),
-                                  buf("workspace", workspace, 1, 1, plan.workspace_bytes), _stream(stream))
+    st = lib().grad_norm_clip_run(plan.handle, max_norm, buf("norm", norm, F32, 1, 1),
+                                  buf("workspace", workspace, _BYTES, 1, plan.workspace_bytes), _stream(stream))
     return _check(st, "grad_norm_clip_run", raise_on_error)
 
 
