@@ -34,7 +34,9 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <memory>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "clip_sum.h"
@@ -367,6 +369,15 @@ struct grad_clip_plan_s {
   std::vector<GcEntry> table;
   int64_t slots;
   uint64_t id;  // 64 bits that no other plan of this process has
+  // What the tensors occupy, by beginning: [begin, the farthest end up to here).
+  std::vector<std::pair<uint64_t, uint64_t>> spans;
+
+  bool touches(const void* p, uint64_t bytes) const {
+    const uint64_t lo = reinterpret_cast<uint64_t>(p), hi = lo + bytes;
+    const auto behind = std::lower_bound(spans.begin(), spans.end(), hi,
+                                         [](const std::pair<uint64_t, uint64_t>& s, uint64_t v) { return s.first < v; });
+    return behind != spans.begin() && (behind - 1)->second > lo;
+  }
 };
 
 static std::atomic<uint64_t> gc_plans{0};
@@ -411,12 +422,14 @@ extern "C" ovl_status grad_clip_plan(const grad_clip_tensor* tensors, int64_t nu
       end_any = std::max(end_any, s.hi);
       if (s.written) end_written = std::max(end_written, s.hi);
     }
-    grad_clip_plan_s* p = new grad_clip_plan_s;
+    std::unique_ptr<grad_clip_plan_s> p(new grad_clip_plan_s);
+    p->spans.reserve(spans.size());
     p->slots = slot;
+    for (const Span& s : spans) p->spans.emplace_back(s.lo, std::max(s.hi, p->spans.empty() ? 0 : p->spans.back().second));
     p->id = (++gc_plans + 1) * 0x9E3779B97F4A7C15ull;  // odd: a bijection of the plan's number
     for (size_t i = 0; i < table.size(); ++i) table[i].tag = gc_tag(table[i], (int64_t)i, p->id);
     p->table.swap(table);
-    *out = p;
+    *out = p.release();
   } catch (const std::bad_alloc&) {
     return OVL_EUNSUPPORTED;
   }
@@ -435,6 +448,7 @@ extern "C" size_t grad_clip_workspace_bytes(grad_clip_plan_t p) {
 extern "C" ovl_status grad_clip_upload(grad_clip_plan_t p, void* workspace, hipStream_t stream) {
   if (!p || !workspace) return OVL_EINVAL;
   if (!aligned16(workspace)) return OVL_EALIGN;
+  if (p->touches(workspace, grad_clip_workspace_bytes(p))) return OVL_EINVAL;
   GcUpload u = {};
   GcEntry* table = reinterpret_cast<GcEntry*>(static_cast<uint8_t*>(workspace) + kGcTable);
   for (size_t i = 0; i < p->table.size(); i += kGcUpload) {
@@ -452,6 +466,9 @@ extern "C" ovl_status grad_norm_clip_run(grad_clip_plan_t p, float max_norm, flo
   if (!p || !norm || !workspace) return OVL_EINVAL;
   if (!(max_norm >= 0.f)) return OVL_EINVAL;  // negative or NaN
   if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(norm) & 3u)) return OVL_EALIGN;
+  const size_t bytes = grad_clip_workspace_bytes(p);
+  const uint64_t at = reinterpret_cast<uint64_t>(norm), ws = reinterpret_cast<uint64_t>(workspace);
+  if ((at < ws + bytes && at + 4 > ws) || p->touches(norm, 4) || p->touches(workspace, bytes)) return OVL_EINVAL;
   DeviceInfo di;
   ovl_status st = current_device_info(&di);
   if (st) return st;

@@ -28,6 +28,25 @@ inline size_t aligned_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The buffers of a call, each with what it is to the call.
+struct CallBuffer {
+  const void* p;
+  bool written;
+};
+// Whether a written buffer begins where another one does, but for the `allowed`
+// pairs of indexes.
+template <size_t N, size_t M>
+inline bool begins_alike(const CallBuffer (&b)[N], const int (&allowed)[M][2]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = i + 1; j < N; ++j) {
+      if (!b[i].p || b[i].p != b[j].p || !(b[i].written || b[j].written)) continue;
+      bool named = false;
+      for (const auto& a : allowed) named |= a[0] == (int)i && a[1] == (int)j;
+      if (!named) return true;
+    }
+  return false;
+}
+
 struct DeviceInfo {
   int device;
   int cus;

@@ -585,7 +585,9 @@ extern "C" ovl_status gemm_epilogue_run(const gemm_epilogue_desc* desc, const vo
     return OVL_EALIGN;
   // In place only where each piece is read by the thread that writes it.
   if (residual == out && (d.res_type != d.out_type || d.ldr != d.ldo)) return OVL_EINVAL;
-  if (z == out || (z && z == residual) || out == a || out == b || (z && (z == a || z == b))) return OVL_EINVAL;
+  const CallBuffer buffers[] = {{residual, false}, {out, true}, {z, true},        {a, false},
+                                {b, false},        {bias, false}, {workspace, true}};
+  if (begins_alike(buffers, {{0, 1}})) return OVL_EINVAL;
   Epilogue e = {};
   e.out = out;
   e.z_out = z;
@@ -656,14 +658,18 @@ extern "C" ovl_status gemm_epilogue_grad_run(const gemm_epilogue_grad_desc* desc
                         static_cast<const void*>(db), db_in, static_cast<const void*>(dbias),
                         static_cast<const void*>(dbias_in)})
     if (!aligned16(p)) return OVL_EALIGN;
+  // (Without rows only db and dbias are written, and what they add is read; z_in
+  // is read for da alone.)
+  const auto rows = [&](const void* p) { return d.m ? p : nullptr; };
+  const CallBuffer buffers[] = {{rows(dy), false}, {rows(z), false}, {rows(dz), dact},  {rows(da ? z_in : nullptr), false},
+                                {rows(da), true},  {db_in, false},   {db, true},        {dbias_in, false},
+                                {dbias, true},     {rows(a), false}, {rows(b), false},  {workspace, true}};
+  if (begins_alike(buffers, {{0, 2}, {1, 2}, {3, 4}, {5, 6}, {7, 8}})) return OVL_EINVAL;
   if (d.m) {
     // In place only where each piece is read by the thread that writes it.
     if (dact && ((dz == dy && (d.dy_type != OVL_BF16 || d.lddy != d.lddz)) || (dz == z && d.ldz != d.lddz)))
       return OVL_EINVAL;
     if (da && da == z_in && (d.da_type != OVL_BF16 || d.ldda != d.ldz_in)) return OVL_EINVAL;
-    for (const void* p : {static_cast<const void*>(da), static_cast<const void*>(db), static_cast<const void*>(dbias)})
-      if (p && (p == dz || p == a || p == b)) return OVL_EINVAL;
-    if ((da && (da == db || da == db_in)) || (dact && (dz == a || dz == b))) return OVL_EINVAL;
   }
   if (dact && d.m) {
     LinDactArgs g = {dy, static_cast<const uint16_t*>(z), static_cast<uint16_t*>(dz), d.lddy, d.ldz, d.lddz,

@@ -774,7 +774,10 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
       !aligned16(out) || !aligned16(router) || (reinterpret_cast<uintptr_t>(topk_idx) & 3u) ||
       (reinterpret_cast<uintptr_t>(gates) & 3u))
     return OVL_EALIGN;
-  if (out == x || out == w1 || out == w2) return OVL_EINVAL;
+  const bool routed = router != nullptr;
+  const CallBuffer buffers[] = {{x, false},        {router, false}, {topk_idx, routed}, {gates, routed}, {w1, false},
+                                {w1_scale, false}, {w2, false},     {w2_scale, false},  {out, true},     {workspace, true}};
+  if (begins_alike(buffers, {{-1, -1}})) return OVL_EINVAL;
   const MoeShape s = moe_shape(*d);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeArgs a = {};

@@ -509,8 +509,8 @@ ovl_status ring_allreduce_run(const ring_desc* desc, const float* const* in, flo
  * (ld*) count elements, 0 standing for a dense row; they are multiples of 8,
  * at most 2^20, and what lies between a row's end and the next row is neither
  * read nor written.  Outputs may not overlap inputs or each other, but for the
- * cases named at each call; one that begins where another such buffer does is
- * refused (EINVAL).
+ * cases named at each call, nor the workspace; one that begins where another
+ * such buffer does is refused (EINVAL).
  * ---------------------------------------------------------------------- */
 enum { OVL_BF16 = 0, OVL_F32 = 1, OVL_FP8 = 2 /* E4M3 codes with scales */ };
 
@@ -670,8 +670,10 @@ size_t grad_clip_workspace_bytes(grad_clip_plan_t plan);
  * norm to NaN and scales nothing. */
 ovl_status grad_clip_upload(grad_clip_plan_t plan, void* workspace, hipStream_t stream);
 
-/* norm: device float32.  max_norm >= 0, infinite for the norm alone (a dst
- * other than src is still written, as a copy).  Errors: EINVAL, EALIGN. */
+/* norm: device float32.  A norm or a workspace that overlaps a tensor of the
+ * plan, or the other, is refused (so is such a workspace at the upload).
+ * max_norm >= 0, infinite for the norm alone (a dst other than src is still
+ * written, as a copy).  Errors: EINVAL, EALIGN. */
 ovl_status grad_norm_clip_run(grad_clip_plan_t plan, float max_norm, float* norm, void* workspace,
                               hipStream_t stream);
 
