@@ -27,6 +27,7 @@
 
 #include "epilogue.h"
 #include "host.h"
+#include "moe_ranges.h"
 #include "rows.h"
 
 namespace ovl {
@@ -38,7 +39,6 @@ constexpr int kMoeRouteRows = 64;    // rows of the router a workgroup sums (128
 constexpr int kMoeRouteTokens = 4;   // tokens of a routing group (1 where there is one)
 // Arrival counters: down tiles, then (expert, up tile).
 constexpr int32_t kMoeDownCounters = 1024;
-constexpr int kMoeGroups = 256;  // workgroups of the experts' launches: one a compute unit
 constexpr int kMoePlanes = 3;    // of h: 24 bits, as many as a float32 has
 
 struct MoeArgs {
@@ -304,19 +304,13 @@ __device__ inline int moe_rows(const MoeArgs& a, const int32_t* ids, int e, int 
   return uniform(n);
 }
 
-// Ranges of k that a launch cuts its items into: as many as shorten its
-// rounds of kMoeGroups items, an item counting its steps and a fixed part
-// (about six steps of start and reduction; four more where the ranges' sums
-// meet in memory).  Lane l weighs l + 1 ranges.
+// Ranges of k that a launch cuts its items into: as many as weigh least.  Lane l
+// weighs l % 16 + 1.
 __device__ inline int moe_ranges(int items, int steps, int most) {
-  const int s = (int)lane_id() % 16 + 1;
-  const int per = (steps + s - 1) / s;
-  int cost = (items * s + kMoeGroups - 1) / kMoeGroups * (per + (s > 1 ? 10 : 6));
-  if (s > most || (s - 1) * per >= steps) cost = INT32_MAX;  // too many, or an empty range
-  int best = cost * 16 >= 0 && cost < INT32_MAX / 32 ? cost * 16 + s - 1 : INT32_MAX;
+  int best = moe_range_weight(items, steps, most, (int)lane_id() % kMoeMostRanges + 1);
 #pragma unroll
-  for (int d = 8; d >= 1; d >>= 1) best = min(best, __shfl_xor(best, d, 64));
-  return uniform(best == INT32_MAX ? 1 : best % 16 + 1);
+  for (int d = kMoeMostRanges / 2; d >= 1; d >>= 1) best = min(best, __shfl_xor(best, d, 64));
+  return uniform(moe_weight_ranges(best));
 }
 
 // The units of a workgroup: its items (expert, column tile, range of k) in
