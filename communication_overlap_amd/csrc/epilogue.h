@@ -13,31 +13,37 @@ __device__ inline float bf16_hi_f(uint32_t w) { return __builtin_bit_cast(float,
 __device__ inline uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 __device__ inline uint32_t bf16_pair(float a, float b) { return bf16_bits(a) | bf16_bits(b) << 16; }
 
-// sigma(x) = 1 / (1 + exp(-x)) and sigma(-x), each to a few float32 steps of
-// itself (2 |x| half steps come from the exponent's rounding): with e = exp(-|x|)
-// = h^2 the greater is r = 1 / (1 + e), the lesser e r.  y times the lesser is
-// taken as (y h) (h r), since e leaves float32's range before y e does.
+// sigma(x) = 1 / (1 + exp(-x)) from q = x log2(e) / 2, to a few float32 steps of
+// itself on either side (2 |x| half steps come from the exponent's rounding): with
+// e = exp(-|x|) = h^2, sigma is r = 1 / (1 + e) or e r, and sigma (1 - sigma) is
+// (h r)^2.  A factor y goes in between h and h r, since e leaves float32's range
+// before y e does.
 struct Sigmoid {
   float h, r;
   bool up;
-  __device__ inline explicit Sigmoid(float x) : up(x > 0.f) {
-    h = __builtin_amdgcn_exp2f(fabsf(x) * (-0.5f * 1.44269504088896341f));
+  __device__ inline explicit Sigmoid(float q) : up(q > 0.f) {
+    h = __builtin_amdgcn_exp2f(-fabsf(q));
     r = __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.f));
   }
+  // y sigma
   __device__ inline float times(float y) const {
     const float g = up ? 1.f : h;
     return (y * g) * (g * r);
   }
-  __device__ inline float complement() const {
-    const float g = up ? h : 1.f;
-    return g * (g * r);
+  // sigma + y sigma (1 - sigma)
+  __device__ inline float slope(float y) const {
+    const float m = h * r;
+    return __builtin_fmaf(y * m, m, up ? r : h * m);
   }
 };
 
+constexpr float kHalfLog2e = 0.721347520444481704f;
 // The tanh form of GELU, 0.5 z (1 + tanh u), u = sqrt(2 / pi) (z + 0.044715 z^3),
-// is z sigma(2 u): no cancellation where tanh is near -1.  2 u from z and z^2:
-constexpr float kGelu1 = 1.59576912160573071f, kGelu3 = 0.044715f * kGelu1;
-__device__ inline float gelu_arg(float z, float z2) { return z * __builtin_fmaf(kGelu3, z2, kGelu1); }
+// is z sigma(2 u): no cancellation where tanh is near -1.  2 u is z times
+constexpr float kGelu1 = 1.59576912160573071f, kGelu3 = 0.044715f * kGelu1;  // kGelu1 + kGelu3 z^2
+__device__ inline float gelu_q(float z, float z2) {
+  return z * __builtin_fmaf(kGelu3 * kHalfLog2e, z2, kGelu1 * kHalfLog2e);
+}
 
 // The normal distribution's tail beyond |z|, exp(-z^2 / 2) r, with r a
 // polynomial in t = 1 / (1 + 0.3 |z|): the scaled complementary error function
@@ -66,8 +72,8 @@ __device__ inline float act_f(float z, int kind) {
       const NormalTail n(z);
       return z * (z > 0.f ? 1.f - n.e * n.r : n.e * n.r);
     }
-    case OVL_ACT_GELU_TANH: return Sigmoid(gelu_arg(z, z * z)).times(z);
-    case OVL_ACT_SILU: return Sigmoid(z).times(z);
+    case OVL_ACT_GELU_TANH: return Sigmoid(gelu_q(z, z * z)).times(z);
+    case OVL_ACT_SILU: return Sigmoid(z * kHalfLog2e).times(z);
     default: return z;
   }
 }
@@ -86,13 +92,10 @@ __device__ inline float act_grad_f(float z, int kind) {
     }
     case OVL_ACT_GELU_TANH: {  // s + z s (1 - s) d(2 u) / dz
       const float z2 = fminf(z * z, 1024.f), v = __builtin_amdgcn_fmed3f(z, -32.f, 32.f);
-      const Sigmoid s(gelu_arg(z, z2));
-      return s.times(1.f + v * s.complement() * __builtin_fmaf(3.f * kGelu3, z2, kGelu1));
+      return Sigmoid(gelu_q(z, z2)).slope(v * __builtin_fmaf(3.f * kGelu3, z2, kGelu1));
     }
-    case OVL_ACT_SILU: {  // s + z s (1 - s)
-      const Sigmoid s(z);
-      return s.times(1.f + __builtin_amdgcn_fmed3f(z, -256.f, 256.f) * s.complement());
-    }
+    case OVL_ACT_SILU:  // s + z s (1 - s)
+      return Sigmoid(z * kHalfLog2e).slope(__builtin_amdgcn_fmed3f(z, -256.f, 256.f));
     default: return 1.f;
   }
 }

@@ -217,7 +217,8 @@ LEAST = 2.0 ** -148
 
 def test_silu_and_its_derivative_keep_their_tails():
     """z sigma(z) down to where it leaves float32, near z = -106, and its
-    derivative s (1 + z (1 - s)), whose inner sum is off by the error of |z| (1 - s)."""
+    derivative s + z s (1 - s): the first term is off by sigma's error, the
+    second, h r squared, by no more of itself, and their sum by U."""
     z = np.linspace(-120, 20, 14001).astype(np.float32)
     v = z.astype(np.float64)
     want = v * sigmoid(v)
@@ -226,7 +227,7 @@ def test_silu_and_its_derivative_keep_their_tails():
     v = z.astype(np.float64)
     s, t = sigmoid(v), sigmoid(-v)
     want = s * (1 + v * t)
-    bound = s * (np.abs(1 + v * t) * sigma_bound(v) + np.abs(v) * t * sigma_bound(v) + fu.U) + LEAST
+    bound = s * (1 + np.abs(v) * t) * sigma_bound(v) + fu.U * np.abs(want) + LEAST
     got = derivative("silu", z)
     closest(got, want, bound, z)
     assert np.abs(got[(z < -80) & (z > -100)]).min() > 0
@@ -248,7 +249,7 @@ def test_gelu_tanh_and_its_derivative_keep_their_tails():
     s, t = sigmoid(w), sigmoid(-w)
     want = s * (1 + v * t * d)
     err = sigma_bound(w) + 7 * np.abs(w) * fu.U
-    bound = s * (np.abs(1 + v * t * d) * err + np.abs(v) * t * d * (err + 8 * fu.U) + fu.U) + LEAST
+    bound = s * (err + np.abs(v) * t * d * (err + 8 * fu.U)) + fu.U * np.abs(want) + LEAST
     closest(derivative("gelu_tanh", z), want, bound, z)
 
 
