@@ -72,10 +72,26 @@ __device__ inline float act_f(float z, int kind) {
       const NormalTail n(z);
       return z * (z > 0.f ? 1.f - n.e * n.r : n.e * n.r);
     }
-    case OVL_ACT_GELU_TANH: return Sigmoid(gelu_q(z, z * z)).times(z);
-    case OVL_ACT_SILU: return Sigmoid(z * kHalfLog2e).times(z);
     default: return z;
   }
+}
+
+// z sigma(x), q = x log2(e) / 2 of eight z: by 1 / (1 + exp(-x)) itself, which is
+// infinity's reciprocal below x = -88 where z sigma(x) still is a number, and
+// from x = -44 down by the other form (for all of them that one takes 3 us more
+// over the 8192 x 3584 outputs of a product with SiLU).
+__device__ inline void times_sigma8(float (&z)[8], const float (&q)[8]) {
+  float least = q[0];
+#pragma unroll
+  for (int c = 1; c < 8; ++c) least = fminf(least, q[c]);
+  float v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] = z[c] * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-2.f * q[c]));
+  if (least < -32.f)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = q[c] < -32.f ? Sigmoid(q[c]).times(z[c]) : v[c];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) z[c] = v[c];
 }
 
 // d act / dz.  A smooth one's factor z is taken at most so far out that the
@@ -109,8 +125,18 @@ __device__ inline void act8(float (&v)[8], int kind) {
   switch (kind) {
     OVL_ACT8(OVL_ACT_RELU)
     OVL_ACT8(OVL_ACT_GELU)
-    OVL_ACT8(OVL_ACT_GELU_TANH)
-    OVL_ACT8(OVL_ACT_SILU)
+    case OVL_ACT_GELU_TANH:
+    case OVL_ACT_SILU: {
+      float q[8];
+      if (kind == OVL_ACT_SILU)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) q[c] = v[c] * kHalfLog2e;
+      else
+#pragma unroll
+        for (int c = 0; c < 8; ++c) q[c] = gelu_q(v[c], v[c] * v[c]);
+      times_sigma8(v, q);
+      break;
+    }
     default: break;
   }
 #undef OVL_ACT8
