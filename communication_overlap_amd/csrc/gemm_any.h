@@ -25,7 +25,7 @@
 // time.
 //
 // Large products are bound by the matrix units at the clock their power
-// allows: 8192 x 3584 x 4096, both sums and epilogue, 229 us (1.05 PFLOP/s),
+// allows: 8192 x 3584 x 4096, both sums and epilogue, 236 us (1.02 PFLOP/s),
 // 207 us (1.16) with a plain store; the library's product alone 197 us.
 #pragma once
 

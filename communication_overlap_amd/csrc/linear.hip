@@ -13,11 +13,14 @@
 // second launch sums them in range order and applies the epilogue.
 //
 // Measured, with what bounds them: forward 8192 x 3584 x 4096 with bias and
-// GELU 229-232 us (matrix units and power); gradient 8192 x 4096 x 1792 232-237 us
-// (the same, 1.04 PFLOP/s over both products); 1000 x 2056 x 520 13 us and the
-// gradient of 700 x 2056 x 520 17 us (latency: a launch, 9 and 17 K steps, an
-// epilogue, a second launch in the latter); 1 x 7168 x 8192 24.2 us (HBM, 117
-// MB at 4.8 TB/s with start and end, which take about 5 us of it).
+// GELU 236 us (matrix units and power); gradient 8192 x 4096 x 1792 239 us (the
+// same, 1.01 PFLOP/s over both products; with the activation of the call's own,
+// a launch before it, 268); 1000 x 2056 x 520 13.3 us and the gradient of 700 x
+// 2056 x 520 16.6 us (latency: a launch, 9 and 11 K steps, an epilogue, a second
+// launch in the latter); 1 x 7168 x 8192 24.3 us (HBM, 117 MB at 4.8 TB/s with
+// start and end, which take about 5 us of it); 1 x 50304 x 4096 74 us and 1 x
+// 36864 x 4096 75 us (HBM at 5.5 and 4.0 TB/s: one workgroup a column tile, 393
+// and 288 of them, so that the second round is half and an eighth full).
 #include <algorithm>
 
 #include "epilogue.h"
@@ -316,8 +319,8 @@ using Da128 = AnyTile<128, 128, 4, true, true>;
 using Db256 = AnyTile<256, 256, 8, false, false>;
 using Db128 = AnyTile<128, 128, 4, false, false>;
 // Few tiles: half the rows, three stages deep, two workgroups a compute unit
-// (1000 x 2056 x 520: 13.5 us against 14.6 with 128 x 128 tiles four deep, the
-// gradient of 128 x 256 x 256 6.1 against 8.5).
+// (1000 x 2056 x 520: 13.5 us against 14.6 with 128 x 128 tiles four deep; the
+// gradient of 128 x 256 x 256, captured, 6.1 against 8.5).
 using Fwd64 = AnyTile<64, 128, 4, true, false, 3>;
 using Da64 = AnyTile<64, 128, 4, true, true, 3>;
 using Db64 = AnyTile<64, 128, 4, false, false, 3>;
@@ -335,9 +338,15 @@ constexpr int kLinCus = 256;  // the plan is made for a whole MI355X, so that si
 
 // What cutting K costs and saves, in microseconds: a step of a 64 x 128 tile,
 // two on a compute unit, a second launch, and a float32 partial product's way
-// to memory and back (8 bytes an element at 4 TB/s).  The costs are fitted:
-// with 128 x 128 tiles 33 x 256 x 1024 ran in 8.7 us cut and 12.8 whole, and
-// 512 x 1024 x 2048 in 20.4 us cut in eight and 15 as this weighs it.
+// to memory and back (8 bytes an element at 4 TB/s).  The operands' own way from
+// memory is not in it, and a gradient without da or db is cut as the whole one.
+// The three are fitted together to the times of calls, and the launch's is not
+// what a trace gives it (4 us, the second kernel's own work included).
+// Captured, us as this cuts and whole: forward 40 x 512 x 4096 12.9 and 27.8,
+// 512 x 1024 x 2048 14.1 and 18.2, 256 x 1024 x 1024 11.2 and 12.3, 256 x 4096 x
+// 1792 16.4 and 17.2; gradient of 700 x 2056 x 520 18.6 and 21.8, of 4000 x 264 x
+// 264 19.1 and 31.1, but of 1000 x 264 x 264 13.7 and 11.1.  With 4 us for the
+// launch the last one runs whole, and so do the two forward ones before.
 constexpr double kLinStepUs = 0.4, kLinLaunchUs = 1.0, kLinPartialUs = 8.0 / 4e6;
 
 LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum_n) {
@@ -362,7 +371,7 @@ LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum
   // the length that costs least.  More of them: a product whose tiles are over
   // half again as long as a compute unit's share of all the work is cut to that
   // share (64 x 7168 x 8192, gradient: 32 tiles of 112 steps beside 896 of one;
-  // 128 us whole, 81 cut).
+  // 183 us whole, 91 cut).
   int64_t len = longest;
   if (s.tile_m == 64) {
     double best = kLinStepUs * longest;
@@ -397,7 +406,8 @@ LinShape lin_shape(const int64_t (*mnk)[3], int jobs, int64_t sum_m, int64_t sum
     if (sp > 1) off += aligned_up((size_t)(sp * mnk[j][0] * mnk[j][1]) * 4, 256);
   }
   // Column sums: a workgroup adds a strip's rows at the latency of its loads, so
-  // few strips are cut into ranges of rows (7936 x 16: 16 us in one).
+  // few strips are cut into ranges of rows (7936 x 16 x 64, gradient: 24 us in one,
+  // 14 cut).
   const int64_t strips = std::max<int64_t>(1, ceil_div(sum_n, 64));
   s.sum_splits = (int32_t)std::max<int64_t>({1, std::min<int64_t>(sum_m / 1024, 64 / strips), std::min<int64_t>(sum_m / 16384, 64)});
   s.sum_off = off;

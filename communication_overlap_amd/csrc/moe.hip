@@ -19,10 +19,11 @@
 // Every workgroup of 2 and 3 lists the distinct experts itself, from the at
 // most 1024 chosen ids, and finds its items' pairs there.
 //
-// Measured (4096 x 1408, 64 experts, gated): one token, top 2, bf16 33.4 us, of
+// Measured (4096 x 1408, 64 experts, gated): one token, top 2, bf16 33.5 us, of
 // which 12 is the 70 MB stream and the rest the three launches' starts and ends;
-// 64 tokens, top 2, bf16 343-360 us (HBM: 1.85 GB, up 5.6 and down 5.4 TB/s); 9
-// tokens, top 4, FP8 101-107 us (HBM: 437 MB, up 4.8 and down 3.9 TB/s).
+// 64 tokens, top 2, bf16 345-368 us (HBM: 1.85 GB, up 5.6 and down 5.4 TB/s), 128
+// tokens 408; 9 tokens, top 4, FP8 92-104 us by how many experts they choose (HBM:
+// 437 MB, up 4.8 and down 4.0 TB/s).
 #include <algorithm>
 
 #include "epilogue.h"
@@ -721,7 +722,7 @@ ovl_status moe_route(const MoeArgs& a, hipStream_t stream) {
 
 // bf16 weights: NB blocks of 16 rows a unit.  Two where experts have many
 // tokens; their rows take a slot from the down launch's ring (64 tokens, top 2
-// of 64: 133 us with two blocks, 113 with one).
+// of 64: 134 us with two blocks, 115 with one).
 template <int NB>
 ovl_status moe_bf16(const MoeArgs& a, bool gated, hipStream_t stream) {
   const ovl_status st = gated ? moe_up<RowCfg<false, true, 1, NB, 1, kMoeRing>>(a, stream)
@@ -808,7 +809,8 @@ extern "C" ovl_status moe_layer_run(const moe_layer_desc* d, const void* x, cons
   a.down_steps = s.down_steps;
   a.chunks = s.chunks;
   // At most one unit a workgroup, and no more tokens than one workgroup sums at
-  // once (40 tokens of 112 columns: 22 us so, 12 with a launch for the sum).
+  // once (40 tokens, 112 x 400, top 4 of 16: 33 us the layer so, 24 with a launch
+  // for the sum).
   a.fused = (int64_t)s.pairs * s.down_tiles <= kMoeGroups && s.pairs <= 8 * d->topk;
   a.pick = router && d->tokens == 1 && d->experts <= 64;
   if (router) {
